@@ -302,6 +302,102 @@ rq_status qjl_attention(const void *q, int64_t G, int n_q, int d, int m, const v
                         float softmax_scale, float *out, void *workspace, size_t workspace_bytes,
                         rq_stream_t stream);
 
+/* ---- Rotary positions -------------------------------------------------------
+ * The keys of the cache are compressed, and the queries projected, after their
+ * rotary positions: the pair (a, b) of a head's values becomes
+ *   scale * (a cos t - b sin t, b cos t + a sin t),   t = position * freq_i,
+ * for i < rot_dim / 2; values rot_dim .. d-1 of the head are copied.
+ * RQ_ROPE_HALF pairs value i with i + rot_dim/2, RQ_ROPE_INTERLEAVED 2i with
+ * 2i + 1.  inverse != 0 takes -t: the gradient of the forward call is the
+ * inverse call (the same scale) on the output's gradient. */
+typedef enum { RQ_ROPE_HALF = 0, RQ_ROPE_INTERLEAVED = 1 } rq_rope_style;
+typedef enum {
+    RQ_ROPE_PLAIN = 0,
+    RQ_ROPE_LINEAR = 1,
+    RQ_ROPE_NTK = 2,
+    RQ_ROPE_YARN = 3,
+    RQ_ROPE_BANDED = 4
+} rq_rope_scaling;
+
+/* Strides, in elements, of a [batch][token][head][d] tensor whose heads are d
+ * contiguous values. */
+typedef struct { int64_t batch, token, head; } rq_strides;
+
+/* Angle per position step of every pair, and the factor on cosine and sine:
+ * freq_out[rot_dim / 2] and *scale_out (HOST, float64).  f_i = theta^(-2i/rot_dim) and
+ *   PLAIN   f_i;
+ *   LINEAR  f_i / factor;
+ *   NTK     theta replaced by theta * factor^(rot_dim / (rot_dim - 2)) (rot_dim > 2);
+ *   YARN    f_i (1 - r_i) + f_i / factor * r_i, r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *           lo = max(floor(at(p0)), 0), hi = min(ceil(at(p1)), rot_dim - 1),
+ *           at(n) = rot_dim ln(original_len / (2 pi n)) / (2 ln theta): p0 >= p1 > 0 are turns over
+ *           the original length (32 and 1 are usual); scale = 0.1 ln(factor) + 1;
+ *   BANDED  f_i (s_i + (1 - s_i) / factor), s_i = clamp((original_len / w_i - p0) / (p1 - p0), 0, 1),
+ *           w_i = 2 pi / f_i, p1 > p0 (4 and 1 are usual).
+ * scale = 1 but for YARN.  rot_dim even, 2 .. 512; theta > 1; factor >= 1; what a kind does not
+ * name is ignored.  Host only. */
+rq_status rq_rotary_frequencies(int rot_dim, double theta, rq_rope_scaling scaling, double factor,
+                                double original_len, double p0, double p1, double *freq_out, double *scale_out);
+
+/* Rotate n_heads heads of x (and, in the same launch, n_heads2 heads of x2:
+ * a token's query and key heads; n_heads2 = 0: none) at positions[b][t].
+ *   x, out (x2, out2): dtype fp16/bf16, [B][n_tok][heads][d] with the given
+ *   strides, aligned to their element at least (16-byte aligned pointers and
+ *   strides of whole 16 bytes give the widest accesses); out may be x with the
+ *   same strides (in place), else they must not overlap.  Writing with other
+ *   strides lays the keys out per head for rq_quantize / qjl_sketch.
+ *   positions: DEVICE int64, batch b at positions + b * pos_batch_stride (0: shared
+ *   by the batch); any value, the angle is reduced exactly (64-bit fixed-point turns).
+ *   freq: HOST, rot_dim / 2 finite float64 (rq_rotary_frequencies, or any).
+ *   d even, 2 .. 512; rot_dim even, 2 .. d; |freq| < 2^20.
+ * Computed in fp32, rounded once. */
+rq_status rq_rotary(const void *x, const rq_strides *x_strides, void *out, const rq_strides *out_strides, int n_heads,
+                    const void *x2, const rq_strides *x2_strides, void *out2, const rq_strides *out2_strides,
+                    int n_heads2, rq_dtype dtype, int64_t B, int64_t n_tok, int d, int rot_dim, rq_rope_style style,
+                    const int64_t *positions, int64_t pos_batch_stride, const double *freq, double scale, int inverse,
+                    rq_stream_t stream);
+
+/* ---- Eviction by accumulated attention weight --------------------------------
+ * Keep the cached tokens that received the most attention: add each step's
+ * softmax weights (of qjl_score's scores) to a sum per token, choose the tokens
+ * with the largest sums, move their records together. */
+
+/* Device workspace rq_evict_accumulate needs (bytes). */
+size_t rq_evict_accumulate_workspace_bytes(int64_t G, int n_q, int64_t T);
+
+/* out[g][t] = decay * acc[g][t] + sum over the group's n_q queries of
+ * softmax over t of (softmax_scale * scores[g][q][t]), in fp32.
+ *   scores fp32 [G][n_q][T] (qjl_score); row_len: int32 [G][n_q], query (g, q)
+ *   sees tokens t < row_len (clamped to 0 .. T), or NULL: all T.  A query that
+ *   sees nothing, or only scores of -inf, adds nothing; what lies behind its
+ *   length is not read as a score (NaN there does no harm).
+ *   acc fp32 [G][T] (not read, and may be NULL, when decay = 0); out fp32
+ *   [G][T], may be acc.  The sum runs in query order: no atomics, so the same
+ *   call gives the same bits. */
+rq_status rq_evict_accumulate(const float *scores, int64_t G, int n_q, int64_t T, const int32_t *row_len,
+                              float softmax_scale, float decay, const float *acc, float *out, void *workspace,
+                              size_t workspace_bytes, rq_stream_t stream);
+
+/* Choose the tokens of each group to keep: of its len[g] tokens (int32 [G],
+ * clamped to 0 .. T; NULL: T) the first n_sink, the last n_recent, and those of
+ * the largest acc (fp32 [G][T]) up to `keep` in all; equal sums in order of the
+ * index, NaN after everything else.  n_sink + n_recent <= keep.
+ *   idx int32 [G][keep]: the kept indices, ascending, then -1;
+ *   count int32 [G] = min(keep, len[g]). */
+rq_status rq_evict_select(const float *acc, int64_t G, int64_t T, const int32_t *len, int keep, int n_sink,
+                          int n_recent, int32_t *idx, int32_t *count, rq_stream_t stream);
+
+/* One array of per-token records: src [G][T][row_bytes] -> dst [G][T_dst][row_bytes] (DEVICE). */
+typedef struct { const void *src; void *dst; int64_t row_bytes; } rq_rows;
+
+/* Move the records of tokens idx[g][0 .. count[g]) (rq_evict_select's, or any)
+ * of every array (HOST array of 1 .. 16 rq_rows: codes, norms, sign bits, sums)
+ * to rows 0 .. count[g] - 1 of dst; rows behind them are left as they were, and
+ * so is the row of an index outside 0 .. T-1.  T_dst >= keep; row_bytes 1 ..
+ * 65536; src and dst of an array must not overlap (RQ_EINVAL). */
+rq_status rq_evict_gather(const int32_t *idx, const int32_t *count, int64_t G, int keep, int64_t T, int64_t T_dst,
+                          const rq_rows *arrays, int n_arrays, rq_stream_t stream);
+
 /* qjl_score without a caller-provided workspace.  The pages have no
  * counterpart to this entry point; it exists for callers that cannot allocate
  * device memory -- a serving engine that reserved all of its HBM for the KV

@@ -11,4 +11,7 @@ from ._lib import (  # noqa: F401
     qjl_sketch_outlier_workspace_bytes, rq_beta_lloyd_max, rq_code_bytes, rq_dequantize, rq_dequantize_dense, rq_device_error, rq_last_launch, rq_lloyd_max, rq_make_rotation, rq_quantize_dense,
     rq_probe_bounded_wait, rq_quantize,
     rq_quantize_qjl, status_string,
+    RQ_ROPE_BANDED, RQ_ROPE_HALF, RQ_ROPE_INTERLEAVED, RQ_ROPE_LINEAR, RQ_ROPE_NTK, RQ_ROPE_PLAIN, RQ_ROPE_YARN,
+    rq_evict_accumulate, rq_evict_accumulate_workspace_bytes, rq_evict_gather, rq_evict_select, rq_rotary,
+    rq_rotary_frequencies,
 )

@@ -8,6 +8,7 @@ missing or unloadable librq.so raises immediately -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -19,9 +20,21 @@ LIB_PATH = os.path.join(_HERE, "librq.so")
 
 RQ_F16, RQ_BF16 = 0, 1
 RQ_CODES_PACKED, RQ_CODES_INT8 = 0, 1
+RQ_ROPE_HALF, RQ_ROPE_INTERLEAVED = 0, 1
+RQ_ROPE_PLAIN, RQ_ROPE_LINEAR, RQ_ROPE_NTK, RQ_ROPE_YARN, RQ_ROPE_BANDED = range(5)
 
 _lock = threading.Lock()
 _lib = None
+
+
+class Strides(C.Structure):
+    """rq_strides: batch, token and head strides in elements."""
+    _fields_ = [("batch", C.c_int64), ("token", C.c_int64), ("head", C.c_int64)]
+
+
+class Rows(C.Structure):
+    """rq_rows: one array of per-token records to move."""
+    _fields_ = [("src", C.c_void_p), ("dst", C.c_void_p), ("row_bytes", C.c_int64)]
 
 
 class RQError(RuntimeError):
@@ -67,6 +80,14 @@ def lib() -> C.CDLL:
                 "rq_make_rotation": (i32, [i32, u64, fp]),
                 "rq_quantize_dense": (i32, [vp, i32, i64, i32, vp, i32, i32, fp, vp, vp, vp]),
                 "rq_dequantize_dense": (i32, [vp, vp, i64, i32, vp, i32, i32, fp, vp, i32, vp]),
+                "rq_rotary_frequencies": (i32, [i32, C.c_double, i32, C.c_double, C.c_double, C.c_double, C.c_double,
+                                                vp, vp]),
+                "rq_rotary": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i64, i64, i32, i32, i32, vp, i64,
+                                    vp, C.c_double, i32, vp]),
+                "rq_evict_accumulate_workspace_bytes": (sz, [i64, i32, i64]),
+                "rq_evict_accumulate": (i32, [vp, i64, i32, i64, vp, C.c_float, C.c_float, vp, vp, vp, sz, vp]),
+                "rq_evict_select": (i32, [vp, i64, i64, vp, i32, i32, i32, vp, vp, vp]),
+                "rq_evict_gather": (i32, [vp, vp, i64, i32, i64, i64, vp, i32, vp]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(L, name)
@@ -82,7 +103,8 @@ def exported_symbols():
             "rq_quantize_qjl", "qjl_make_projection", "qjl_sketch", "qjl_score_workspace_bytes", "qjl_score",
             "qjl_score_noalloc", "qjl_attention_workspace_bytes", "qjl_attention", "rq_beta_lloyd_max",
             "rq_make_rotation", "rq_quantize_dense", "rq_dequantize_dense", "qjl_sketch_outlier_workspace_bytes",
-            "qjl_sketch_outlier", "qjl_score_outlier"]
+            "qjl_sketch_outlier", "qjl_score_outlier", "rq_rotary_frequencies", "rq_rotary",
+            "rq_evict_accumulate_workspace_bytes", "rq_evict_accumulate", "rq_evict_select", "rq_evict_gather"]
 
 
 def status_string(status: int) -> str:
@@ -271,3 +293,87 @@ def qjl_score_noalloc(q, G, n_q, d, m, proj, signs, sk_norms, T, scores, codes=N
     _check("qjl_score_noalloc", lib().qjl_score_noalloc(
         _dev(q), G, n_q, d, m, _dev(proj), _dtype_code(proj), _dev(signs), _dev(sk_norms), T, _dev(codes),
         _dev(norms), bits, layout, int(use_signs), sign_seed, cp, _dev(scores), _stream(stream)))
+
+
+def _on(t, stream):
+    """Context in which `t`'s device is current: a call without a stream runs on the current stream of its
+    tensors' device, also when another device is current."""
+    if stream is not None or t.device.index is None:
+        return contextlib.nullcontext()
+    import torch
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _strides(t, what):
+    """rq_strides of a [batch][token][head][d] tensor with contiguous heads."""
+    s = t.stride()
+    if len(s) != 4 or (s[3] != 1 and t.shape[3] != 1):
+        raise ValueError(f"{what}: expected a [batch, token, head, d] tensor with contiguous heads")
+    return Strides(s[0], s[1], s[2])
+
+
+def rq_rotary_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = RQ_ROPE_PLAIN, factor: float = 1.0,
+                          original_len: float = 1.0, p0: float = 0.0, p1: float = 0.0):
+    """(freq float64 [rot_dim / 2], scale): angle per position step of every pair, and the factor on cos and sin."""
+    out, scale = np.zeros(max(1, rot_dim // 2), np.float64), C.c_double(0.0)
+    _check("rq_rotary_frequencies", lib().rq_rotary_frequencies(rot_dim, theta, scaling, factor, original_len, p0, p1,
+                                                                out.ctypes.data, C.addressof(scale)))
+    return out, scale.value
+
+
+def rq_rotary(x, out, positions, freq, rot_dim, style, scale=1.0, inverse=False, x2=None, out2=None, stream=None):
+    """Rotate the heads of x [B, n_tok, heads, d] (and of x2, in the same launch) into out (out2); positions int64
+    [B, n_tok] (batch stride 0: shared).  out may be x."""
+    import torch
+    f = np.ascontiguousarray(np.asarray(freq, dtype=np.float64))
+    B, n, H, d = x.shape
+    if f.size < rot_dim // 2 or out.shape != x.shape or positions.dtype != torch.int64 or \
+            tuple(positions.shape) != (B, n) or (n > 1 and positions.stride(1) != 1):
+        raise ValueError("rq_rotary: freq [rot_dim / 2], out of x's shape, positions int64 [B, n_tok] expected")
+    two = x2 is not None
+    if two and (out2 is None or out2.shape != x2.shape or tuple(x2.shape[:2]) != (B, n) or x2.shape[3] != d or
+                x2.dtype != x.dtype or out2.dtype != x.dtype):
+        raise ValueError("rq_rotary: x2 and out2 of x's batch, tokens, d and dtype expected")
+    if out.dtype != x.dtype:
+        raise TypeError("rq_rotary: out has another dtype than x")
+    s = [_strides(x, "x"), _strides(out, "out")] + ([_strides(x2, "x2"), _strides(out2, "out2")] if two else [])
+    p = [C.addressof(v) for v in s] + [None] * (4 - len(s))
+    with _on(x, stream):
+        _check("rq_rotary", lib().rq_rotary(
+            _dev(x), p[0], _dev(out), p[1], H, _dev(x2), p[2], _dev(out2), p[3], x2.shape[2] if two else 0,
+            _dtype_code(x), B, n, d, rot_dim, style, _dev(positions), positions.stride(0), f.ctypes.data, float(scale),
+            int(bool(inverse)), _stream(stream)))
+
+
+def rq_evict_accumulate_workspace_bytes(G, n_q, T) -> int:
+    return lib().rq_evict_accumulate_workspace_bytes(G, n_q, T)
+
+
+def rq_evict_accumulate(scores, G, n_q, T, softmax_scale, decay, acc, out, workspace, row_len=None, stream=None):
+    """out [G][T] = decay * acc + sum over queries of softmax(softmax_scale * scores [G][n_q][T])."""
+    with _on(out, stream):
+        _check("rq_evict_accumulate", lib().rq_evict_accumulate(
+            _dev(scores), G, n_q, T, _dev(row_len), float(softmax_scale), float(decay), _dev(acc), _dev(out),
+            _dev(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _stream(stream)))
+
+
+def rq_evict_select(acc, G, T, keep, idx, count, length=None, n_sink=0, n_recent=0, stream=None):
+    """idx int32 [G][keep]: the tokens to keep of each group, ascending, then -1; count int32 [G]."""
+    with _on(idx, stream):
+        _check("rq_evict_select", lib().rq_evict_select(_dev(acc), G, T, _dev(length), keep, n_sink, n_recent,
+                                                        _dev(idx), _dev(count), _stream(stream)))
+
+
+def rq_evict_gather(idx, count, G, keep, T, arrays, T_dst=None, stream=None):
+    """Move the records idx [G][keep] of every (src [G][T]..., dst [G][T_dst]...) pair of contiguous tensors."""
+    rows = (Rows * len(arrays))()
+    T_dst = keep if T_dst is None else T_dst
+    for r, (src, dst) in zip(rows, arrays):
+        r.src, r.dst = src.data_ptr(), dst.data_ptr()
+        r.row_bytes = src.numel() * src.element_size() // max(1, G * T)
+        if dst.numel() * dst.element_size() != r.row_bytes * G * T_dst:
+            raise ValueError("rq_evict_gather: dst does not hold [G][T_dst] records of src's size")
+    with _on(idx, stream):
+        _check("rq_evict_gather", lib().rq_evict_gather(_dev(idx), _dev(count), G, keep, T, T_dst, C.addressof(rows),
+                                                        len(arrays), _stream(stream)))

@@ -15,7 +15,7 @@
 #include <cuda_runtime.h>
 
 #include "rq.h"
-#include "rq_kernels.h"
+#include "rq_cache_ops.h"
 
 using rq::QuantTables;
 
@@ -932,6 +932,176 @@ rq_status qjl_score_outlier(const void *q, int64_t G, int n_q, int d, int m, con
                                              static_cast<const uint16_t *>(proj), out_idx, out_signs, out_norms,
                                              scores, reinterpret_cast<cudaStream_t>(stream));
     return cuda_status(e);
+}
+
+// ------------------------------------------------------------------ rotary positions
+
+rq_status rq_rotary_frequencies(int rot_dim, double theta, rq_rope_scaling scaling, double factor, double original_len,
+                                double p0, double p1, double *freq_out, double *scale_out)
+{
+    if (rot_dim < 2 || rot_dim > rq::kMaxRot || rot_dim % 2 || !freq_out || !scale_out) return RQ_EINVAL;
+    if (!(theta > 1.0) || !std::isfinite(theta)) return RQ_EINVAL;
+    if (scaling < RQ_ROPE_PLAIN || scaling > RQ_ROPE_BANDED) return RQ_EINVAL;
+    const bool longer = scaling == RQ_ROPE_YARN || scaling == RQ_ROPE_BANDED;
+    if (scaling != RQ_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return RQ_EINVAL;
+    if (longer && (!(original_len > 0.0) || !std::isfinite(original_len) || !std::isfinite(p0) || !std::isfinite(p1)))
+        return RQ_EINVAL;
+    if (scaling == RQ_ROPE_YARN && !(p0 >= p1 && p1 > 0.0)) return RQ_EINVAL;
+    if (scaling == RQ_ROPE_BANDED && !(p1 > p0)) return RQ_EINVAL;
+    if (scaling == RQ_ROPE_NTK && rot_dim == 2) return RQ_EINVAL;
+    const double two_pi = 6.283185307179586476925286766559;
+    const double base = scaling == RQ_ROPE_NTK ? theta * std::pow(factor, rot_dim / (rot_dim - 2.0)) : theta;
+    double lo = 0.0, hi = 0.0;
+    if (scaling == RQ_ROPE_YARN) {
+        lo = std::fmax(std::floor(rot_dim * std::log(original_len / (p0 * two_pi)) / (2.0 * std::log(theta))), 0.0);
+        hi = std::fmin(std::ceil(rot_dim * std::log(original_len / (p1 * two_pi)) / (2.0 * std::log(theta))), rot_dim - 1.0);
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == RQ_ROPE_LINEAR) f /= factor;
+        if (scaling == RQ_ROPE_YARN) {
+            const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            f = f * (1.0 - r) + f / factor * r;
+        }
+        if (scaling == RQ_ROPE_BANDED) {
+            const double s = std::fmin(std::fmax((original_len * f / two_pi - p0) / (p1 - p0), 0.0), 1.0);
+            f = f * s + f / factor * (1.0 - s);
+        }
+        freq_out[i] = f;
+    }
+    *scale_out = scaling == RQ_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return RQ_OK;
+}
+
+static rq_status rotary_tensor(const void *in, const rq_strides *is, void *out, const rq_strides *os, int heads,
+                               int64_t B, int64_t n_tok, rq::RotaryTensor &t)
+{
+    if (!in || !is || !out || !os) return RQ_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 1u) return RQ_EALIGN;
+    t.in = static_cast<const uint16_t *>(in);
+    t.out = static_cast<uint16_t *>(out);
+    // the stride of a dimension of one element is never used
+    t.in_batch = B > 1 ? is->batch : 0; t.in_token = n_tok > 1 ? is->token : 0; t.in_head = heads > 1 ? is->head : 0;
+    t.out_batch = B > 1 ? os->batch : 0; t.out_token = n_tok > 1 ? os->token : 0; t.out_head = heads > 1 ? os->head : 0;
+    return RQ_OK;
+}
+
+rq_status rq_rotary(const void *x, const rq_strides *x_strides, void *out, const rq_strides *out_strides, int n_heads,
+                    const void *x2, const rq_strides *x2_strides, void *out2, const rq_strides *out2_strides,
+                    int n_heads2, rq_dtype dtype, int64_t B, int64_t n_tok, int d, int rot_dim, rq_rope_style style,
+                    const int64_t *positions, int64_t pos_batch_stride, const double *freq, double scale, int inverse,
+                    rq_stream_t stream)
+{
+    rq::begin_call();
+    if (dtype != RQ_F16 && dtype != RQ_BF16) return RQ_EINVAL;
+    if (style != RQ_ROPE_HALF && style != RQ_ROPE_INTERLEAVED) return RQ_EINVAL;
+    if (B < 0 || n_tok < 0 || n_heads < 1 || n_heads2 < 0) return RQ_EINVAL;
+    if (d < 2 || d > rq::kMaxRot || d % 2 || rot_dim < 2 || rot_dim > d || rot_dim % 2) return RQ_EINVAL;
+    if (!freq || !std::isfinite(scale) || std::fabs(scale) > 1e30) return RQ_EINVAL;
+    for (int i = 0; i < rot_dim / 2; ++i)
+        if (!(std::fabs(freq[i]) < 1048576.0)) return RQ_EINVAL;
+    if (n_heads > 65535 || n_heads2 > 65535 || B > 0x7fffffff || n_tok > 0x7fffffff || B * n_tok > 0x7fffffff)
+        return RQ_ESIZE;
+    if (B == 0 || n_tok == 0) return RQ_OK;
+    if (!positions) return RQ_EINVAL;
+    if (reinterpret_cast<uintptr_t>(positions) & 7u) return RQ_EALIGN;
+    rq::RotaryArgs a{};
+    rq_status s = rotary_tensor(x, x_strides, out, out_strides, n_heads, B, n_tok, a.x);
+    if (s) return s;
+    if (n_heads2 > 0) {
+        s = rotary_tensor(x2, x2_strides, out2, out2_strides, n_heads2, B, n_tok, a.x2);
+        if (s) return s;
+    }
+    auto in_place = [](const rq::RotaryTensor &t) {
+        return t.in == t.out && t.in_batch == t.out_batch && t.in_token == t.out_token && t.in_head == t.out_head;
+    };
+    a.copy = rot_dim < d && !(in_place(a.x) && (n_heads2 == 0 || in_place(a.x2)));
+    a.n_heads = n_heads; a.n_heads2 = n_heads2; a.B = B; a.n_tok = n_tok; a.d = d; a.rot = rot_dim;
+    a.bf16 = dtype == RQ_BF16; a.half = style == RQ_ROPE_HALF; a.inverse = inverse != 0;
+    a.positions = positions; a.pos_batch_stride = B > 1 ? pos_batch_stride : 0; a.scale = (float)scale;
+    a.num_sms = num_sms();
+    if (a.num_sms <= 0) return RQ_ECUDA;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        // freq / 2 pi modulo 1 in 0.64 fixed point (80-bit long double: 64 significant bits)
+        const long double turn = (long double)freq[i] / 6.283185307179586476925286766559005768L;
+        const long double frac = turn - floorl(turn);
+        const long double fixed = frac * 18446744073709551616.0L;
+        a.turns[i] = fixed >= 18446744073709551615.0L ? 0ull : (uint64_t)(fixed + 0.5L);
+    }
+    return cuda_status(rq::launch_rotary(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ eviction
+
+size_t rq_evict_accumulate_workspace_bytes(int64_t G, int n_q, int64_t T)
+{
+    if (G <= 0 || n_q <= 0 || T <= 0) return 0;
+    return rq::accumulate_workspace_bytes(G, n_q, T);
+}
+
+rq_status rq_evict_accumulate(const float *scores, int64_t G, int n_q, int64_t T, const int32_t *row_len,
+                              float softmax_scale, float decay, const float *acc, float *out, void *workspace,
+                              size_t workspace_bytes, rq_stream_t stream)
+{
+    rq::begin_call();
+    if (G < 0 || n_q < 0 || T < 0) return RQ_EINVAL;
+    if (!(softmax_scale >= 0.0f) || softmax_scale > 1e30f || !std::isfinite(decay)) return RQ_EINVAL;
+    if (G > 65535 || n_q > 4096 || T > ((int64_t)1 << 31)) return RQ_ESIZE;
+    if (G == 0 || T == 0) return RQ_OK;
+    if (!out || (!acc && decay != 0.0f)) return RQ_EINVAL;
+    if (n_q > 0 && (!scores || !workspace)) return RQ_EINVAL;
+    if (workspace_bytes < rq_evict_accumulate_workspace_bytes(G, n_q, T)) return RQ_ESIZE;
+    if (!aligned16(scores) || !aligned16(row_len) || !aligned16(acc) || !aligned16(out) || !aligned16(workspace))
+        return RQ_EALIGN;
+    rq::AccumulateArgs a{};
+    a.scores = scores; a.G = G; a.T = T; a.nq = n_q; a.row_len = row_len; a.scale = softmax_scale; a.decay = decay;
+    a.acc = acc; a.out = out; a.workspace = static_cast<float *>(workspace); a.num_sms = num_sms();
+    if (a.num_sms <= 0) return RQ_ECUDA;
+    return cuda_status(rq::launch_accumulate(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rq_status rq_evict_select(const float *acc, int64_t G, int64_t T, const int32_t *len, int keep, int n_sink,
+                          int n_recent, int32_t *idx, int32_t *count, rq_stream_t stream)
+{
+    rq::begin_call();
+    if (G < 0 || T < 0 || keep < 1 || n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > keep) return RQ_EINVAL;
+    if (G > 65535 || T > ((int64_t)1 << 28) || keep > (1 << 28)) return RQ_ESIZE;
+    if (G == 0) return RQ_OK;
+    if ((!acc && T > 0) || !idx || !count) return RQ_EINVAL;
+    if (!aligned16(acc) || !aligned16(len) || !aligned16(idx) || !aligned16(count)) return RQ_EALIGN;
+    rq::SelectArgs a{};
+    a.acc = acc; a.G = G; a.T = T; a.len = len; a.keep = keep; a.n_sink = n_sink; a.n_recent = n_recent; a.idx = idx;
+    a.count = count; a.num_sms = num_sms();
+    if (a.num_sms <= 0) return RQ_ECUDA;
+    return cuda_status(rq::launch_select(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+rq_status rq_evict_gather(const int32_t *idx, const int32_t *count, int64_t G, int keep, int64_t T, int64_t T_dst,
+                          const rq_rows *arrays, int n_arrays, rq_stream_t stream)
+{
+    rq::begin_call();
+    if (G < 0 || keep < 1 || T < 0 || T_dst < keep || n_arrays < 1 || n_arrays > rq::kMaxRowArrays || !arrays)
+        return RQ_EINVAL;
+    if (G > 65535 || T > ((int64_t)1 << 31) || T_dst > ((int64_t)1 << 31) || keep > (1 << 28)) return RQ_ESIZE;
+    for (int i = 0; i < n_arrays; ++i)
+        if (arrays[i].row_bytes < 1 || arrays[i].row_bytes > 65536) return RQ_EINVAL;
+    if (G == 0 || T == 0) return RQ_OK;
+    if (!idx || !count) return RQ_EINVAL;
+    if (!aligned16(idx) || !aligned16(count)) return RQ_EALIGN;
+    rq::GatherArgs a{};
+    for (int i = 0; i < n_arrays; ++i) {
+        const rq_rows &r = arrays[i];
+        if (!r.src || !r.dst) return RQ_EINVAL;
+        if (!aligned16(r.src) || !aligned16(r.dst)) return RQ_EALIGN;
+        const uintptr_t s0 = reinterpret_cast<uintptr_t>(r.src), d0 = reinterpret_cast<uintptr_t>(r.dst);
+        const uintptr_t sn = (uintptr_t)G * T * r.row_bytes, dn = (uintptr_t)G * T_dst * r.row_bytes;
+        if (s0 < d0 + dn && d0 < s0 + sn) return RQ_EINVAL;
+        a.src[i] = static_cast<const uint8_t *>(r.src);
+        a.dst[i] = static_cast<uint8_t *>(r.dst);
+        a.row_bytes[i] = r.row_bytes;
+    }
+    a.idx = idx; a.count = count; a.G = G; a.T = T; a.T_dst = T_dst; a.keep = keep; a.n_arrays = n_arrays;
+    return cuda_status(rq::launch_gather(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

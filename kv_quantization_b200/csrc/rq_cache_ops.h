@@ -1,0 +1,65 @@
+// rq_cache_ops.h -- internal launch interface of the decode-side cache operators: rotary positions, tree attention
+// over the compressed cache, eviction by accumulated attention weight.
+#pragma once
+#include "rq_kernels.h"
+
+namespace rq {
+
+// Rotary positions (rq_rotary.cu).
+struct RotaryTensor {
+    const uint16_t *in;        // nullptr: absent (n_heads2 = 0)
+    uint16_t *out;
+    int64_t in_batch, in_token, in_head, out_batch, out_token, out_head;   // strides in elements
+};
+constexpr int kMaxRot = 512;
+struct RotaryArgs {
+    RotaryTensor x, x2;
+    int n_heads, n_heads2;
+    int64_t B, n_tok;
+    int d, rot;
+    bool bf16, half, inverse, copy;    // copy: the d - rot unrotated values have to be written
+    const int64_t *positions;
+    int64_t pos_batch_stride;
+    float scale;
+    int num_sms;
+    int items, hs, tb, heads_per_block;   // launch shape (set by launch_rotary)
+    uint64_t turns[kMaxRot / 2];       // freq_i / 2 pi modulo 1, 0.64 fixed point
+};
+cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t st);
+
+// Eviction from a cache by accumulated attention weight (rq_evict.cu).
+struct AccumulateArgs {
+    const float *scores;       // [G][nq][T]
+    int64_t G, T;
+    int nq;
+    const int32_t *row_len;    // [G][nq] or nullptr
+    float scale, decay;
+    const float *acc;          // [G][T]
+    float *out;
+    float *workspace;
+    int num_sms;
+};
+size_t accumulate_workspace_bytes(int64_t G, int nq, int64_t T);
+cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t st);
+struct SelectArgs {
+    const float *acc;          // [G][T]
+    int64_t G, T;
+    const int32_t *len;        // [G] or nullptr
+    int keep, n_sink, n_recent;
+    int32_t *idx;              // [G][keep]
+    int32_t *count;            // [G]
+    int num_sms;
+};
+cudaError_t launch_select(const SelectArgs &a, cudaStream_t st);
+constexpr int kMaxRowArrays = 16;
+struct GatherArgs {
+    const int32_t *idx, *count;
+    int64_t G, T, T_dst;
+    int keep, n_arrays;
+    const uint8_t *src[kMaxRowArrays];
+    uint8_t *dst[kMaxRowArrays];
+    int64_t row_bytes[kMaxRowArrays];
+};
+cudaError_t launch_gather(const GatherArgs &a, cudaStream_t st);
+
+}  // namespace rq

@@ -1,0 +1,172 @@
+"""Host side of the decode-side cache operators: refusals before anything is enqueued, and the rotary frequencies
+against their formulas (no GPU)."""
+import ctypes as C
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_quantization_b200 import _lib as L
+
+EINVAL, EALIGN, ESIZE, EUNSUPPORTED = -1, -2, -3, -4
+ST = L.Strides(0, 0, 0)
+A = 0x100000                                                   # a device address that is never dereferenced
+
+
+def rotary_status(**kw):
+    a = dict(x=A, xs=ST, out=A, os=ST, heads=2, x2=None, x2s=None, out2=None, o2s=None, heads2=0, dtype=L.RQ_BF16, B=1,
+             n=1, d=128, rot=128, style=L.RQ_ROPE_HALF, pos=A, ps=0, freq=np.ones(256), scale=1.0, inverse=0)
+    a.update(kw)
+    ref = lambda s: None if s is None else C.addressof(s)  # noqa: E731
+    return L.lib().rq_rotary(a["x"], ref(a["xs"]), a["out"], ref(a["os"]), a["heads"], a["x2"], ref(a["x2s"]),
+                             a["out2"], ref(a["o2s"]), a["heads2"], a["dtype"], a["B"], a["n"], a["d"], a["rot"],
+                             a["style"], a["pos"], a["ps"],
+                             None if a["freq"] is None else a["freq"].ctypes.data, a["scale"], a["inverse"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(dtype=2), EINVAL), (dict(style=2), EINVAL), (dict(B=-1), EINVAL), (dict(n=-1), EINVAL),
+    (dict(heads=0), EINVAL), (dict(heads2=-1), EINVAL), (dict(d=127), EINVAL), (dict(d=514, rot=2), EINVAL),
+    (dict(rot=3), EINVAL), (dict(rot=0), EINVAL), (dict(d=64, rot=66), EINVAL), (dict(freq=None), EINVAL),
+    (dict(freq=np.full(256, np.nan)), EINVAL), (dict(freq=np.full(256, 2.0 ** 20)), EINVAL),
+    (dict(scale=math.inf), EINVAL), (dict(x=None), EINVAL), (dict(out=None), EINVAL), (dict(xs=None), EINVAL),
+    (dict(pos=None), EINVAL), (dict(heads2=1), EINVAL), (dict(x=A + 1), EALIGN), (dict(pos=A + 4), EALIGN),
+    (dict(n=1 << 31), ESIZE), (dict(B=1 << 16, n=1 << 16), ESIZE), (dict(heads=70000), ESIZE),
+])
+def test_rotary_refuses(kw, status):
+    assert rotary_status(**kw) == status
+    assert L.rq_last_launch() == ""
+
+
+def test_rotary_of_no_tokens_is_a_noop():
+    assert rotary_status(B=0, x=None, pos=None) == 0
+    assert rotary_status(n=0, x=None, pos=None) == 0
+
+
+def test_rotary_binding_checks_shapes():
+    x = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(2, 3, dtype=torch.int64)
+    f = np.ones(32)
+    for bad in (lambda: L.rq_rotary(x, x[:, :2], pos, f, 64, 0), lambda: L.rq_rotary(x, x, pos.int(), f, 64, 0),
+                lambda: L.rq_rotary(x, x, pos[:, :2], f, 64, 0), lambda: L.rq_rotary(x, x, pos, f[:8], 64, 0),
+                lambda: L.rq_rotary(x.transpose(2, 3), x.transpose(2, 3), pos, f, 64, 0),
+                lambda: L.rq_rotary(x, x, pos, f, 64, 0, x2=x[:1], out2=x[:1]),
+                lambda: L.rq_rotary(x, x, pos, f, 64, 0, x2=x)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        L.rq_rotary(x, x.half(), pos, f, 64, 0)
+    with pytest.raises(TypeError):
+        L.rq_rotary(x.float(), x.float(), pos, f, 64, 0, stream=0)
+
+
+def formula(rot, theta, kind, factor, length, p0, p1):
+    f = np.array([theta ** (-2.0 * i / rot) for i in range(rot // 2)])
+    if kind == L.RQ_ROPE_LINEAR:
+        return f / factor
+    if kind == L.RQ_ROPE_NTK:
+        return np.array([(theta * factor ** (rot / (rot - 2))) ** (-2.0 * i / rot) for i in range(rot // 2)])
+    if kind == L.RQ_ROPE_YARN:
+        at = lambda turns: rot * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(theta))  # noqa: E731
+        lo, hi = max(math.floor(at(p0)), 0), min(math.ceil(at(p1)), rot - 1)
+        r = np.clip((np.arange(rot // 2) - lo) / max(hi - lo, 1e-3), 0, 1)
+        return f / factor * r + f * (1 - r)
+    if kind == L.RQ_ROPE_BANDED:
+        s = np.clip((length / (2 * math.pi / f) - p0) / (p1 - p0), 0, 1)
+        return (1 - s) * f / factor + s * f
+    return f
+
+
+@pytest.mark.parametrize("kind, args", [(L.RQ_ROPE_PLAIN, (1.0, 1.0, 0.0, 0.0)), (L.RQ_ROPE_LINEAR, (4.0, 1.0, 0.0, 0.0)),
+                                        (L.RQ_ROPE_NTK, (8.0, 1.0, 0.0, 0.0)), (L.RQ_ROPE_YARN, (16.0, 4096.0, 32.0, 1.0)),
+                                        (L.RQ_ROPE_BANDED, (8.0, 8192.0, 1.0, 4.0))])
+@pytest.mark.parametrize("rot, theta", [(128, 10000.0), (64, 500000.0), (20, 10000.0), (512, 1e6), (4, 100.0)])
+def test_frequencies(kind, args, rot, theta):
+    f, scale = L.rq_rotary_frequencies(rot, theta, kind, *args)
+    assert f.shape == (rot // 2,)
+    assert np.allclose(f, formula(rot, theta, kind, *args), rtol=1e-13, atol=0)
+    assert scale == pytest.approx(0.1 * math.log(args[0]) + 1.0 if kind == L.RQ_ROPE_YARN else 1.0, rel=1e-15)
+
+
+def test_frequency_scaling_does_what_it_is_for():
+    plain, _ = L.rq_rotary_frequencies(128)
+    yarn, _ = L.rq_rotary_frequencies(128, 10000.0, L.RQ_ROPE_YARN, 8.0, 4096.0, 32.0, 1.0)
+    band, _ = L.rq_rotary_frequencies(128, 10000.0, L.RQ_ROPE_BANDED, 8.0, 8192.0, 1.0, 4.0)
+    ntk, _ = L.rq_rotary_frequencies(128, 10000.0, L.RQ_ROPE_NTK, 8.0)
+    for f in (yarn, band):                                     # fast pairs as they were, slow ones interpolated
+        assert f[0] == plain[0] and f[-1] == pytest.approx(plain[-1] / 8.0, rel=1e-12)
+    assert ntk[0] == 1.0 and ntk[-1] == pytest.approx(plain[-1] / 8.0, rel=1e-12)
+
+
+@pytest.mark.parametrize("args", [
+    (0,), (3,), (514,), (64, 1.0), (64, math.inf), (64, 1e4, 5), (64, 1e4, L.RQ_ROPE_LINEAR, 0.5),
+    (64, 1e4, L.RQ_ROPE_YARN, 2.0, 0.0, 32.0, 1.0), (64, 1e4, L.RQ_ROPE_YARN, 2.0, 4096.0, 1.0, 32.0),
+    (64, 1e4, L.RQ_ROPE_BANDED, 2.0, 4096.0, 4.0, 1.0), (64, 1e4, L.RQ_ROPE_BANDED, 2.0, math.nan, 1.0, 4.0),
+    (2, 1e4, L.RQ_ROPE_NTK, 2.0),
+])
+def test_frequencies_refuse(args):
+    with pytest.raises(L.RQError) as e:
+        L.rq_rotary_frequencies(*args)
+    assert e.value.status == EINVAL
+
+
+def accumulate_status(**kw):
+    a = dict(scores=A, G=2, nq=3, T=5, row_len=None, scale=1.0, decay=1.0, acc=A, out=A, ws=A, wsb=1 << 20)
+    a.update(kw)
+    return L.lib().rq_evict_accumulate(a["scores"], a["G"], a["nq"], a["T"], a["row_len"], a["scale"], a["decay"],
+                                       a["acc"], a["out"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(G=-1), EINVAL), (dict(nq=-1), EINVAL), (dict(T=-1), EINVAL), (dict(scale=-1.0), EINVAL),
+    (dict(scale=math.nan), EINVAL), (dict(decay=math.inf), EINVAL), (dict(scores=None), EINVAL),
+    (dict(acc=None), EINVAL), (dict(out=None), EINVAL), (dict(ws=None), EINVAL), (dict(wsb=0), ESIZE),
+    (dict(G=65536), ESIZE), (dict(nq=4097), ESIZE), (dict(T=(1 << 31) + 1), ESIZE), (dict(scores=A + 4), EALIGN),
+    (dict(row_len=A + 4), EALIGN), (dict(out=A + 8), EALIGN), (dict(ws=A + 8), EALIGN),
+])
+def test_accumulate_refuses(kw, status):
+    assert accumulate_status(**kw) == status
+
+
+def test_accumulate_of_nothing_is_a_noop():
+    assert accumulate_status(G=0, scores=None, acc=None, out=None, ws=None, wsb=0) == 0
+    assert accumulate_status(T=0, scores=None, acc=None, out=None, ws=None, wsb=0) == 0
+    assert L.rq_evict_accumulate_workspace_bytes(0, 4, 100) == 0
+    assert L.rq_evict_accumulate_workspace_bytes(2, 4, 100) > 0
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(G=-1), EINVAL), (dict(T=-1), EINVAL), (dict(keep=0), EINVAL), (dict(sink=-1), EINVAL),
+    (dict(recent=-1), EINVAL), (dict(sink=3, recent=6), EINVAL), (dict(acc=None), EINVAL), (dict(idx=None), EINVAL),
+    (dict(count=None), EINVAL), (dict(idx=A + 4), EALIGN), (dict(acc=A + 4), EALIGN), (dict(G=65536), ESIZE),
+    (dict(T=(1 << 28) + 1), ESIZE), (dict(keep=(1 << 28) + 1), ESIZE),
+])
+def test_select_refuses(kw, status):
+    a = dict(acc=A, G=2, T=20, len=None, keep=8, sink=0, recent=0, idx=A, count=A)
+    a.update(kw)
+    assert L.lib().rq_evict_select(a["acc"], a["G"], a["T"], a["len"], a["keep"], a["sink"], a["recent"], a["idx"],
+                                   a["count"], None) == status
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(G=-1), EINVAL), (dict(keep=0), EINVAL), (dict(T_dst=7), EINVAL), (dict(n=0), EINVAL), (dict(n=17), EINVAL),
+    (dict(row=0), EINVAL), (dict(row=65537), EINVAL), (dict(idx=None), EINVAL), (dict(src=None), EINVAL),
+    (dict(dst=None), EINVAL), (dict(src=A + 8), EALIGN), (dict(dst=A + 0x100008), EALIGN), (dict(dst=A), EINVAL),
+    (dict(dst=A + 2 * 20 * 16 - 16), EINVAL), (dict(dst=A - 2 * 8 * 16 + 16), EINVAL), (dict(G=65536), ESIZE),
+])
+def test_gather_refuses(kw, status):
+    a = dict(idx=A, count=A, G=2, keep=8, T=20, T_dst=8, src=A, dst=A + 0x100000, row=16, n=1)
+    a.update(kw)
+    rows = (L.Rows * 17)()
+    for r in rows:
+        r.src, r.dst, r.row_bytes = a["src"], a["dst"], a["row"]
+    assert L.lib().rq_evict_gather(a["idx"], a["count"], a["G"], a["keep"], a["T"], a["T_dst"], C.addressof(rows),
+                                   a["n"], None) == status
+
+
+def test_gather_binding_checks_sizes():
+    src, dst = torch.zeros(2, 20, 3), torch.zeros(2, 7, 3)
+    with pytest.raises(ValueError):
+        L.rq_evict_gather(torch.zeros(2, 8, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 2, 8, 20,
+                          [(src, dst)], stream=0)
