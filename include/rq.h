@@ -357,6 +357,48 @@ rq_status rq_rotary(const void *x, const rq_strides *x_strides, void *out, const
                     const int64_t *positions, int64_t pos_batch_stride, const double *freq, double scale, int inverse,
                     rq_stream_t stream);
 
+/* ---- Attention of drafted tokens (and the decode step) -------------------------
+ * A tree of n_nodes drafted tokens per sequence, not yet in the cache, attends
+ * to the sequence's compressed cache and, in 16 bits, to the drafted tokens
+ * themselves, under one softmax.  Row (b, i, h) -- node i, query head h of key
+ * head h / n_rep -- sees the first kv_len cached tokens of group g = b *
+ * n_kv_heads + h / n_rep and the nodes j whose bit its mask row has:
+ *   out = softmax over both of (softmax_scale * s) applied to both kinds of values,
+ * s = the qjl_score estimator for a cached token, <q, k_new_j> for a drafted
+ * one; the cached values are rq_dequantize's before rounding (as qjl_attention).
+ * A row that sees nothing gives 0.  One node is the ordinary decode step: the
+ * new token beside a cache of ragged lengths.
+ *   q, out: bf16 [B][n_nodes][n_kv_heads * n_rep][d]; k_new, v_new: bf16
+ *   [B][n_nodes][n_kv_heads][d]; any strides of whole 16 bytes (rq_rotary's
+ *   outputs, or views of a projection's); out must not overlap the inputs.
+ *   tree_mask: uint64 [n_nodes][ceil(n_nodes / 64)], bit j % 64 of word j / 64 of
+ *   row i set: node i sees node j; batch b at tree_mask + b * mask_batch_stride
+ *   (words; 0: one tree for all).  NULL: a chain (j <= i).  Keys and values that
+ *   no row sees may hold anything.
+ *   proj .. centroids, v_codes .. v_centroids: as qjl_attention, the cache arrays
+ *   [G][T] with G = B * n_kv_heads and T the cache's capacity; kv_len: int32 [G],
+ *   clamped to 0 .. T, or NULL: T.  T = 0: the cache pointers may be NULL.
+ *   workspace: qjl_tree_attention_workspace_bytes(...) bytes (overwritten); calls
+ *   (or captured graphs) that may run at the same time need one each.
+ * Arithmetic as qjl_attention; the drafted part, sums and joins in fp32; the
+ * output is rounded once.
+ * Supported: d = 128, m % 64 == 0, codes of 1, 2, 3, 4 bits packed or int8, values
+ * likewise (RQ_EUNSUPPORTED otherwise); n_nodes <= 1024. */
+
+/* Device workspace qjl_tree_attention needs (bytes), for the current device; 0 on invalid sizes. */
+size_t qjl_tree_attention_workspace_bytes(int64_t B, int n_kv_heads, int n_rep, int n_nodes, int d, int m, int64_t T);
+
+rq_status qjl_tree_attention(const void *q, const rq_strides *q_strides, const void *k_new, const rq_strides *k_strides,
+                             const void *v_new, const rq_strides *v_strides, int64_t B, int n_kv_heads, int n_rep,
+                             int n_nodes, int d, const uint64_t *tree_mask, int64_t mask_batch_stride, int m,
+                             const void *proj, rq_dtype proj_dtype, const uint8_t *signs, const uint16_t *sk_norms,
+                             int64_t T, const int32_t *kv_len, const void *codes, const uint16_t *norms, int bits,
+                             rq_layout layout, int use_signs, uint64_t sign_seed, const float *centroids,
+                             const void *v_codes, const uint16_t *v_norms, int v_bits, rq_layout v_layout,
+                             int v_use_signs, uint64_t v_sign_seed, const float *v_centroids, float softmax_scale,
+                             void *out, const rq_strides *out_strides, void *workspace, size_t workspace_bytes,
+                             rq_stream_t stream);
+
 /* ---- Eviction by accumulated attention weight --------------------------------
  * Keep the cached tokens that received the most attention: add each step's
  * softmax weights (of qjl_score's scores) to a sum per token, choose the tokens

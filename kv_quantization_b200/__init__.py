@@ -12,6 +12,7 @@ from ._lib import (  # noqa: F401
     rq_probe_bounded_wait, rq_quantize,
     rq_quantize_qjl, status_string,
     RQ_ROPE_BANDED, RQ_ROPE_HALF, RQ_ROPE_INTERLEAVED, RQ_ROPE_LINEAR, RQ_ROPE_NTK, RQ_ROPE_PLAIN, RQ_ROPE_YARN,
+    qjl_tree_attention, qjl_tree_attention_workspace_bytes,
     rq_evict_accumulate, rq_evict_accumulate_workspace_bytes, rq_evict_gather, rq_evict_select, rq_rotary,
     rq_rotary_frequencies,
 )

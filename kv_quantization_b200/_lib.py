@@ -84,6 +84,10 @@ def lib() -> C.CDLL:
                                                 vp, vp]),
                 "rq_rotary": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i64, i64, i32, i32, i32, vp, i64,
                                     vp, C.c_double, i32, vp]),
+                "qjl_tree_attention_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32, i64]),
+                "qjl_tree_attention": (i32, [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, i64, i32, vp, i32, vp,
+                                             vp, i64, vp, vp, vp, i32, i32, i32, u64, vp, vp, vp, i32, i32, i32, u64,
+                                             vp, C.c_float, vp, vp, vp, sz, vp]),
                 "rq_evict_accumulate_workspace_bytes": (sz, [i64, i32, i64]),
                 "rq_evict_accumulate": (i32, [vp, i64, i32, i64, vp, C.c_float, C.c_float, vp, vp, vp, sz, vp]),
                 "rq_evict_select": (i32, [vp, i64, i64, vp, i32, i32, i32, vp, vp, vp]),
@@ -104,6 +108,7 @@ def exported_symbols():
             "qjl_score_noalloc", "qjl_attention_workspace_bytes", "qjl_attention", "rq_beta_lloyd_max",
             "rq_make_rotation", "rq_quantize_dense", "rq_dequantize_dense", "qjl_sketch_outlier_workspace_bytes",
             "qjl_sketch_outlier", "qjl_score_outlier", "rq_rotary_frequencies", "rq_rotary",
+            "qjl_tree_attention_workspace_bytes", "qjl_tree_attention",
             "rq_evict_accumulate_workspace_bytes", "rq_evict_accumulate", "rq_evict_select", "rq_evict_gather"]
 
 
@@ -377,3 +382,40 @@ def rq_evict_gather(idx, count, G, keep, T, arrays, T_dst=None, stream=None):
     with _on(idx, stream):
         _check("rq_evict_gather", lib().rq_evict_gather(_dev(idx), _dev(count), G, keep, T, T_dst, C.addressof(rows),
                                                         len(arrays), _stream(stream)))
+
+
+def qjl_tree_attention_workspace_bytes(B, n_kv_heads, n_rep, n_nodes, d, m, T) -> int:
+    return lib().qjl_tree_attention_workspace_bytes(B, n_kv_heads, n_rep, n_nodes, d, m, T)
+
+
+def qjl_tree_attention(q, k_new, v_new, tree_mask, m, proj, signs, sk_norms, T, kv_len, v_codes, v_norms, v_bits,
+                       v_centroids, out, workspace, softmax_scale, codes=None, norms=None, bits=0,
+                       layout=RQ_CODES_PACKED, use_signs=0, sign_seed=0, centroids=None, v_layout=RQ_CODES_PACKED,
+                       v_use_signs=0, v_sign_seed=0, stream=None):
+    """Attention of drafted tokens q [B, n_nodes, heads, d] over the compressed cache and over k_new, v_new
+    [B, n_nodes, kv_heads, d]; tree_mask int64 [B or 1, n_nodes, words] (None: a chain); out bf16 of q's shape."""
+    import torch
+    B, n, H, d = q.shape
+    kv = k_new.shape[2]
+    if tuple(k_new.shape) != (B, n, kv, d) or v_new.shape != k_new.shape or out.shape != q.shape or kv < 1 or H % kv:
+        raise ValueError("qjl_tree_attention: k_new, v_new [B, n_nodes, kv_heads, d] and out of q's shape expected")
+    if any(t.dtype != torch.bfloat16 for t in (q, k_new, v_new, out)):
+        raise TypeError("qjl_tree_attention: bfloat16 q, k_new, v_new and out expected")
+    stride = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, B) or \
+                tuple(tree_mask.shape[1:]) != (n, (n + 63) // 64) or tree_mask.element_size() != 8 or \
+                not tree_mask.is_contiguous():
+            raise ValueError("qjl_tree_attention: contiguous 64-bit tree_mask [B or 1, n_nodes, ceil(n_nodes / 64)] expected")
+        stride = tree_mask.stride(0) if tree_mask.shape[0] > 1 else 0
+    s = [_strides(t, w) for t, w in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out"))]
+    p = [C.addressof(v) for v in s]
+    c = None if centroids is None else np.ascontiguousarray(np.asarray(centroids, dtype=np.float32))
+    vc = np.ascontiguousarray(np.asarray(v_centroids, dtype=np.float32))
+    with _on(q, stream):
+        _check("qjl_tree_attention", lib().qjl_tree_attention(
+            _dev(q), p[0], _dev(k_new), p[1], _dev(v_new), p[2], B, kv, H // kv, n, d, _dev(tree_mask), stride, m,
+            _dev(proj), _dtype_code(proj), _dev(signs), _dev(sk_norms), T, _dev(kv_len), _dev(codes), _dev(norms), bits,
+            layout, int(use_signs), sign_seed, None if c is None else c.ctypes.data, _dev(v_codes), _dev(v_norms), v_bits,
+            v_layout, int(v_use_signs), v_sign_seed, vc.ctypes.data, float(softmax_scale), _dev(out), p[3],
+            _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))

@@ -1,0 +1,95 @@
+// qjl_tree.cu -- launcher of the attention of drafted tokens over the compressed cache (kernels in qjl_tree.cuh).
+#include "qjl_tree.cuh"
+
+namespace rq {
+
+namespace {
+
+int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
+
+// Query rows a block: 32 or 64 when that holds the group's rows; above, 128 (fewer passes over the cache, twice the
+// products per unpacked key) where the operand of kb columns leaves room for two weight buffers in shared memory.
+int tree_nb(int rows, int kb) { return rows <= 32 ? 32 : (rows <= 64 || kb > 384 ? 64 : 128); }
+
+int64_t tree_grid(int64_t G, int rbs, int64_t T, int num_sms)
+{
+    const int64_t items = G * rbs * ((T + kTrTok - 1) / kTrTok);
+    return items < num_sms ? items : num_sms;
+}
+
+template <int NB>
+cudaError_t launch_main(const TreeArgs &a, const QuantTables &tk, const QuantTables &tv, int grid, cudaStream_t st)
+{
+    const int cfg[][2] = {{2, 5}, {2, 3}, {1, 5}, {1, 3}};       // weight buffers, log2 of the lookup tables' copies
+    for (const auto &c : cfg) {
+        const size_t smem = tr_smem(NB, a.kb, a.pw, a.vpw, c[0], 1 << c[1]);
+        if (smem > kMaxSmemPerBlock) continue;
+        cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        tree_attention_kernel<NB><<<(unsigned)grid, kTrThreads, smem, st>>>(a, tk, tv, c[0], c[1]);
+        note_launch("tree_attention_kernel");
+        return cudaGetLastError();
+    }
+    return cudaErrorNotSupported;
+}
+
+struct Plan {
+    int kb, nb, rbs;
+    int64_t q, c, off, part, bytes;
+};
+
+Plan tree_plan(int64_t G, int rows, int64_t T, int m, bool two, int num_sms)
+{
+    Plan p;
+    p.kb = m + (two ? kTrD : 0);
+    p.nb = tree_nb(rows, p.kb);
+    p.rbs = (rows + p.nb - 1) / p.nb;
+    p.q = 0;
+    p.c = up256(p.q + G * p.rbs * p.nb * (int64_t)p.kb * 2);
+    p.off = up256(p.c + G * p.rbs * p.nb * (int64_t)sizeof(float));
+    p.part = up256(p.off + (G + 1) * (int64_t)sizeof(int64_t));
+    p.bytes = p.part + (tree_grid(G, p.rbs, T, num_sms) + G * p.rbs) * (int64_t)(tr_part_floats(p.nb) * sizeof(float));
+    return p;
+}
+
+}  // namespace
+
+bool tree_supported(int d, int m, int pw, int vpw)
+{
+    if (d != kTrD || m % 64 || m < 64 || m > 512) return false;
+    if (!(pw == 0 || pw == 1 || pw == 2 || pw == 3 || pw == 4 || pw == 8)) return false;
+    return vpw == 1 || vpw == 2 || vpw == 3 || vpw == 4 || vpw == 8;
+}
+
+size_t tree_workspace_bytes(int64_t G, int rows, int64_t T, int m, bool two, int num_sms)
+{
+    return (size_t)tree_plan(G, rows, T, m, two, num_sms).bytes;
+}
+
+cudaError_t launch_tree(const TreeArgs &in, const QuantTables &tk, const QuantTables &tv, void *workspace, cudaStream_t st)
+{
+    TreeArgs a = in;
+    const Plan p = tree_plan(a.G, a.rows, a.T, a.m, a.pw != 0, a.num_sms);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.nb = p.nb; a.rbs = p.rbs; a.kb = p.kb;
+    a.wsQ = ws + p.q;
+    a.wsC = reinterpret_cast<float *>(ws + p.c);
+    a.off = reinterpret_cast<int64_t *>(ws + p.off);
+    a.part = reinterpret_cast<float *>(ws + p.part);
+    const int grid = (int)tree_grid(a.G, a.rbs, a.T, a.num_sms);
+    if (grid > 0) {
+        tree_prologue_kernel<<<dim3((unsigned)(a.G * a.rbs * (a.nb / 32)), (unsigned)(a.kb / 64)), 128, 0, st>>>(a, tk);
+        note_launch("tree_prologue_kernel");
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        e = a.nb == 32 ? launch_main<32>(a, tk, tv, grid, st)
+                       : a.nb == 64 ? launch_main<64>(a, tk, tv, grid, st) : launch_main<128>(a, tk, tv, grid, st);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 cgrid((unsigned)((a.rows + kTrCombineRows - 1) / kTrCombineRows), (unsigned)a.G);
+    tree_combine_kernel<<<cgrid, kTrD, (size_t)kTrCombineRows * a.nodes * sizeof(float), st>>>(a, tv, grid);
+    note_launch("tree_combine_kernel");
+    return cudaGetLastError();
+}
+
+}  // namespace rq

@@ -1104,4 +1104,93 @@ rq_status rq_evict_gather(const int32_t *idx, const int32_t *count, int64_t G, i
     return cuda_status(rq::launch_gather(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ attention of drafted tokens
+
+size_t qjl_tree_attention_workspace_bytes(int64_t B, int n_kv_heads, int n_rep, int n_nodes, int d, int m, int64_t T)
+{
+    if (B <= 0 || n_kv_heads <= 0 || n_rep <= 0 || n_nodes <= 0 || d <= 0 || m <= 0 || T < 0) return 0;
+    if (B > 65535 || n_kv_heads > 65535 || n_rep > 65535 || n_nodes > rq::kTreeMaxNodes) return 0;
+    const int sms = num_sms(), rows = n_rep * n_nodes;
+    const size_t one = rq::tree_workspace_bytes(B * n_kv_heads, rows, T, m, false, sms > 0 ? sms : 1);
+    const size_t two = rq::tree_workspace_bytes(B * n_kv_heads, rows, T, m, true, sms > 0 ? sms : 1);
+    return one > two ? one : two;
+}
+
+// A strided bf16 [B][n][heads][d] tensor: non-null, 16-byte aligned rows.
+static rq_status tree_tensor(const void *p, const rq_strides *s, int64_t B, int64_t n, int64_t heads, rq::rq_strides_t &o)
+{
+    if (!p || !s) return RQ_EINVAL;
+    o.batch = B > 1 ? s->batch : 0;                         // the stride of a dimension of one element is never used
+    o.token = n > 1 ? s->token : 0;
+    o.head = heads > 1 ? s->head : 0;
+    if (!aligned16(p) || (o.batch | o.token | o.head) % 8) return RQ_EALIGN;
+    return RQ_OK;
+}
+
+rq_status qjl_tree_attention(const void *q, const rq_strides *q_strides, const void *k_new, const rq_strides *k_strides,
+                             const void *v_new, const rq_strides *v_strides, int64_t B, int n_kv_heads, int n_rep,
+                             int n_nodes, int d, const uint64_t *tree_mask, int64_t mask_batch_stride, int m,
+                             const void *proj, rq_dtype proj_dtype, const uint8_t *signs, const uint16_t *sk_norms,
+                             int64_t T_len, const int32_t *kv_len, const void *codes, const uint16_t *norms, int bits,
+                             rq_layout layout, int use_signs, uint64_t sign_seed, const float *centroids,
+                             const void *v_codes, const uint16_t *v_norms, int v_bits, rq_layout v_layout,
+                             int v_use_signs, uint64_t v_sign_seed, const float *v_centroids, float softmax_scale,
+                             void *out, const rq_strides *out_strides, void *workspace, size_t workspace_bytes,
+                             rq_stream_t stream)
+{
+    rq::begin_call();
+    if (!pow2_d(d)) return RQ_EINVAL;
+    if (m < 8 || m > 512 || m % 8) return RQ_EINVAL;
+    if (proj_dtype != RQ_F16 && proj_dtype != RQ_BF16) return RQ_EINVAL;
+    if (B < 0 || n_kv_heads < 1 || n_rep < 1 || n_nodes < 1 || T_len < 0) return RQ_EINVAL;
+    if (!(softmax_scale >= 0.0f) || softmax_scale > 1e30f) return RQ_EINVAL;
+    if (n_nodes > rq::kTreeMaxNodes || n_rep > 65535 || n_rep * n_nodes > 65536 || n_kv_heads > 65535 || B > 65535 ||
+        B * n_kv_heads > 65535 || T_len > ((int64_t)1 << 31))
+        return RQ_ESIZE;
+    rq_status s = check_common(0, d, v_bits, v_layout);
+    if (s) return s;
+    if (codes) {
+        s = check_common(0, d, bits, layout);
+        if (s) return s;
+    }
+    const int pw = codes ? (layout == RQ_CODES_INT8 ? 8 : bits) : 0, vpw = v_layout == RQ_CODES_INT8 ? 8 : v_bits;
+    if (!rq::tree_supported(d, m, pw, vpw)) return RQ_EUNSUPPORTED;
+    if (B == 0) return RQ_OK;
+    if (!proj || !workspace) return RQ_EINVAL;
+    if (T_len > 0 && (!signs || !sk_norms || !v_codes || !v_norms || (codes && !norms))) return RQ_EINVAL;
+    rq::TreeArgs a{};
+    const int64_t heads = (int64_t)n_kv_heads * n_rep;
+    s = tree_tensor(q, q_strides, B, n_nodes, heads, a.qs);
+    if (s) return s;
+    s = tree_tensor(k_new, k_strides, B, n_nodes, n_kv_heads, a.ks);
+    if (s) return s;
+    s = tree_tensor(v_new, v_strides, B, n_nodes, n_kv_heads, a.vs);
+    if (s) return s;
+    s = tree_tensor(out, out_strides, B, n_nodes, heads, a.os);
+    if (s) return s;
+    if (!aligned16(proj) || !aligned16(signs) || !aligned16(sk_norms) || !aligned16(kv_len) || !aligned16(codes) ||
+        !aligned16(norms) || !aligned16(v_codes) || !aligned16(v_norms) || !aligned16(tree_mask) || !aligned16(workspace))
+        return RQ_EALIGN;
+    QuantTables T, TV;
+    std::memset(&T, 0, sizeof(T));
+    if (codes) {
+        s = tables_for(centroids, bits, d, use_signs, sign_seed, T);
+        if (s) return s;
+    }
+    s = tables_for(v_centroids, v_bits, d, v_use_signs, v_sign_seed, TV);
+    if (s) return s;
+    a.q = static_cast<const uint16_t *>(q); a.k_new = static_cast<const uint16_t *>(k_new);
+    a.v_new = static_cast<const uint16_t *>(v_new); a.out = static_cast<uint16_t *>(out);
+    a.B = B; a.G = B * n_kv_heads; a.T = T_len; a.kv_heads = n_kv_heads; a.rep = n_rep; a.nodes = n_nodes;
+    a.rows = n_rep * n_nodes; a.mask = tree_mask; a.mask_batch = mask_batch_stride; a.m = m;
+    a.proj = static_cast<const uint16_t *>(proj); a.proj_bf16 = proj_dtype == RQ_BF16; a.signs = signs;
+    a.sk_norms = sk_norms; a.kv_len = kv_len; a.codes = static_cast<const uint8_t *>(codes); a.norms = norms; a.pw = pw;
+    a.vcodes = static_cast<const uint8_t *>(v_codes); a.vnorms = v_norms; a.vpw = vpw;
+    a.qscale = softmax_scale * 1.4426950408889634074f;       // log2(e)
+    a.num_sms = num_sms();
+    if (a.num_sms <= 0) return RQ_ECUDA;
+    if (workspace_bytes < rq::tree_workspace_bytes(a.G, a.rows, T_len, m, codes != nullptr, a.num_sms)) return RQ_ESIZE;
+    return cuda_status(rq::launch_tree(a, T, TV, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -62,4 +62,40 @@ struct GatherArgs {
 };
 cudaError_t launch_gather(const GatherArgs &a, cudaStream_t st);
 
+// Attention of drafted tokens over the compressed cache (qjl_tree.cuh).
+struct rq_strides_t { int64_t batch, token, head; };
+struct TreeArgs {
+    const uint16_t *q, *k_new, *v_new;     // bf16 [B][nodes][kv_heads rep or kv_heads][128]
+    uint16_t *out;
+    rq_strides_t qs, ks, vs, os;           // strides in elements
+    int64_t B, G, T;
+    int kv_heads, rep, nodes, rows;        // rows = nodes rep of a group
+    const uint64_t *mask;                  // [nodes][words], batch b at mask + b mask_batch; nullptr: a chain
+    int64_t mask_batch;
+    int m;
+    const uint16_t *proj;
+    bool proj_bf16;
+    const uint8_t *signs;                  // [G][T][m/8]
+    const uint16_t *sk_norms;
+    const int32_t *kv_len;                 // [G] or nullptr
+    const uint8_t *codes;                  // first-stage codes, with norms (pw = 0: pure sketch keys)
+    const uint16_t *norms;
+    int pw;
+    const uint8_t *vcodes;
+    const uint16_t *vnorms;
+    int vpw;
+    float qscale;                          // softmax scale in units of log2
+    int num_sms;
+    // set by tree_plan / launch_tree
+    int nb, rbs, kb;                       // query rows a block, row blocks a group, score operand width
+    uint8_t *wsQ;                          // operand images [G rbs][kb / 64][nb][128 B]
+    float *wsC;                            // [G rbs][nb] |q| qscale
+    int64_t *off;                          // [G + 1] prefix sums of the groups' tiles
+    float *part;
+};
+constexpr int kTreeMaxNodes = 1024;
+bool tree_supported(int d, int m, int pw, int vpw);
+size_t tree_workspace_bytes(int64_t G, int rows, int64_t T, int m, bool two, int num_sms);
+cudaError_t launch_tree(const TreeArgs &a, const QuantTables &tk, const QuantTables &tv, void *workspace, cudaStream_t st);
+
 }  // namespace rq

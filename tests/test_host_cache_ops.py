@@ -170,3 +170,60 @@ def test_gather_binding_checks_sizes():
     with pytest.raises(ValueError):
         L.rq_evict_gather(torch.zeros(2, 8, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 2, 8, 20,
                           [(src, dst)], stream=0)
+
+
+def tree_status(**kw):
+    a = dict(q=A, k=A, v=A, B=1, kv=1, rep=2, n=3, d=128, mask=None, mb=0, m=128, proj=A, pd=L.RQ_BF16, signs=A, sk=A,
+             T=10, lens=None, codes=None, norms=None, bits=0, layout=0, cent=None, vc=A, vn=A, vb=4, vl=0,
+             vcent=L.rq_lloyd_max(4), scale=1.0, out=A, ws=A, wsb=1 << 40, s=ST, os=ST)
+    a.update(kw)
+    ref = lambda x: None if x is None else C.addressof(x)  # noqa: E731
+    tab = lambda x: None if x is None else x.ctypes.data  # noqa: E731
+    return L.lib().qjl_tree_attention(
+        a["q"], ref(a["s"]), a["k"], C.addressof(ST), a["v"], C.addressof(ST), a["B"], a["kv"], a["rep"], a["n"], a["d"],
+        a["mask"], a["mb"], a["m"], a["proj"], a["pd"], a["signs"], a["sk"], a["T"], a["lens"], a["codes"], a["norms"],
+        a["bits"], a["layout"], 0, 0, tab(a["cent"]), a["vc"], a["vn"], a["vb"], a["vl"], 0, 0, tab(a["vcent"]),
+        a["scale"], a["out"], ref(a["os"]), a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(d=96), EINVAL), (dict(d=64), EUNSUPPORTED), (dict(m=12), EINVAL), (dict(m=96), EUNSUPPORTED),
+    (dict(m=520), EINVAL), (dict(pd=3), EINVAL), (dict(B=-1), EINVAL), (dict(kv=0), EINVAL), (dict(rep=0), EINVAL),
+    (dict(n=0), EINVAL), (dict(T=-1), EINVAL), (dict(scale=-1.0), EINVAL), (dict(scale=math.nan), EINVAL),
+    (dict(n=1025), ESIZE), (dict(n=1000, rep=100), ESIZE), (dict(B=70000), ESIZE), (dict(B=300, kv=300), ESIZE),
+    (dict(vb=0), EINVAL), (dict(vb=9), EINVAL), (dict(vb=5), EUNSUPPORTED), (dict(vl=7), EINVAL),
+    (dict(codes=A, norms=A, bits=5, cent=L.rq_lloyd_max(5)), EUNSUPPORTED), (dict(codes=A, bits=2), EINVAL),
+    (dict(codes=A, norms=A, bits=2), EINVAL), (dict(proj=None), EINVAL), (dict(ws=None), EINVAL),
+    (dict(signs=None), EINVAL), (dict(vn=None), EINVAL), (dict(q=None), EINVAL), (dict(out=None), EINVAL),
+    (dict(s=None), EINVAL), (dict(os=None), EINVAL), (dict(q=A + 8), EALIGN), (dict(out=A + 2), EALIGN),
+    (dict(signs=A + 8), EALIGN), (dict(lens=A + 4), EALIGN), (dict(mask=A + 8), EALIGN), (dict(ws=A + 8), EALIGN),
+    (dict(s=L.Strides(0, 4, 0)), EALIGN), (dict(os=L.Strides(0, 0, 130)), EALIGN), (dict(vcent=None), EINVAL),
+    (dict(vcent=L.rq_lloyd_max(4)[::-1].copy()), EINVAL),
+])
+def test_tree_refuses(kw, status):
+    assert tree_status(**kw) == status
+    assert L.rq_last_launch() == ""
+
+
+def test_tree_of_no_sequences_is_a_noop():
+    assert tree_status(B=0, q=None, ws=None) == 0
+
+
+def test_tree_workspace_covers_both_kinds_of_keys():
+    size = L.qjl_tree_attention_workspace_bytes
+    assert size(0, 1, 1, 1, 128, 128, 10) == 0 and size(1, 1, 1, 2000, 128, 128, 10) == 0
+    assert 0 < size(1, 1, 1, 1, 128, 128, 0) < size(1, 1, 1, 1, 128, 128, 5000)
+
+
+def test_tree_binding_checks_shapes():
+    q, k = torch.zeros(2, 3, 4, 128, dtype=torch.bfloat16), torch.zeros(2, 3, 2, 128, dtype=torch.bfloat16)
+    ws = torch.zeros(16, dtype=torch.uint8)
+    f = lambda q=q, k=k, v=k, mask=None, out=q: L.qjl_tree_attention(  # noqa: E731
+        q, k, v, mask, 128, q, None, None, 0, None, None, None, 4, L.rq_lloyd_max(4), out, ws, 1.0, stream=0)
+    for bad in (lambda: f(k=k[:, :2]), lambda: f(v=k[:1]), lambda: f(out=q[:, :2]), lambda: f(q=q[:, :, :3], out=q[:, :, :3]),
+                lambda: f(mask=torch.zeros(2, 3, dtype=torch.int64)), lambda: f(mask=torch.zeros(3, 3, 1, dtype=torch.int64)),
+                lambda: f(mask=torch.zeros(2, 3, 1, dtype=torch.int32)), lambda: f(q=q.transpose(2, 3), out=q.transpose(2, 3))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        f(q=q.half())
