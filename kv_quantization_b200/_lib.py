@@ -8,9 +8,9 @@ missing or unloadable librq.so raises immediately -- there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
+import struct
 import threading
 
 import numpy as np
@@ -300,21 +300,45 @@ def qjl_score_noalloc(q, G, n_q, d, m, proj, signs, sk_norms, T, scores, codes=N
         _dev(norms), bits, layout, int(use_signs), sign_seed, cp, _dev(scores), _stream(stream)))
 
 
-def _on(t, stream):
-    """Context in which `t`'s device is current: a call without a stream runs on the current stream of its
-    tensors' device, also when another device is current."""
-    if stream is not None or t.device.index is None:
-        return contextlib.nullcontext()
-    import torch
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, t, stream, args):
+    """Call `name` with `args` and a stream; without one, the current stream of the device of tensor `t`, also when
+    another device is current."""
+    fn = getattr(_lib or lib(), name)
+    if stream is not None:
+        status = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    else:
+        import torch
+        index = t.device.index
+        raw = torch.cuda.current_stream(index).cuda_stream
+        if index is None or index == torch.cuda.current_device():
+            status = fn(*args, raw)
+        else:
+            with torch.cuda.device(index):
+                status = fn(*args, raw)
+    if status != 0:
+        raise RQError(name, status)
+
+
+_pack3 = struct.Struct("3q").pack
 
 
 def _strides(t, what):
-    """rq_strides of a [batch][token][head][d] tensor with contiguous heads."""
+    """rq_strides (as bytes) of a [batch][token][head][d] tensor with contiguous heads."""
     s = t.stride()
     if len(s) != 4 or (s[3] != 1 and t.shape[3] != 1):
         raise ValueError(f"{what}: expected a [batch, token, head, d] tensor with contiguous heads")
-    return Strides(s[0], s[1], s[2])
+    return _pack3(s[0], s[1], s[2])
+
+
+def _host(a, dtype):
+    """A contiguous host array of dtype (the array itself where it is one)."""
+    if type(a) is np.ndarray and a.dtype == dtype and a.flags.c_contiguous:
+        return a
+    return np.ascontiguousarray(np.asarray(a, dtype=dtype))
 
 
 def rq_rotary_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = RQ_ROPE_PLAIN, factor: float = 1.0,
@@ -330,24 +354,25 @@ def rq_rotary(x, out, positions, freq, rot_dim, style, scale=1.0, inverse=False,
     """Rotate the heads of x [B, n_tok, heads, d] (and of x2, in the same launch) into out (out2); positions int64
     [B, n_tok] (batch stride 0: shared).  out may be x."""
     import torch
-    f = np.ascontiguousarray(np.asarray(freq, dtype=np.float64))
-    B, n, H, d = x.shape
-    if f.size < rot_dim // 2 or out.shape != x.shape or positions.dtype != torch.int64 or \
-            tuple(positions.shape) != (B, n) or (n > 1 and positions.stride(1) != 1):
+    f = _host(freq, np.float64)
+    shape = x.shape
+    B, n, H, d = shape
+    ps = positions.stride()
+    if f.size < rot_dim // 2 or out.shape != shape or positions.dtype != torch.int64 or positions.shape != (B, n) or \
+            (n > 1 and ps[1] != 1):
         raise ValueError("rq_rotary: freq [rot_dim / 2], out of x's shape, positions int64 [B, n_tok] expected")
-    two = x2 is not None
-    if two and (out2 is None or out2.shape != x2.shape or tuple(x2.shape[:2]) != (B, n) or x2.shape[3] != d or
-                x2.dtype != x.dtype or out2.dtype != x.dtype):
-        raise ValueError("rq_rotary: x2 and out2 of x's batch, tokens, d and dtype expected")
+    H2, p2 = 0, (None, None, None, None)
+    if x2 is not None:
+        shape2 = x2.shape
+        if out2 is None or out2.shape != shape2 or shape2[0] != B or shape2[1] != n or shape2[3] != d or \
+                x2.dtype != x.dtype or out2.dtype != x.dtype:
+            raise ValueError("rq_rotary: x2 and out2 of x's batch, tokens, d and dtype expected")
+        H2, p2 = shape2[2], (x2.data_ptr(), _strides(x2, "x2"), out2.data_ptr(), _strides(out2, "out2"))
     if out.dtype != x.dtype:
         raise TypeError("rq_rotary: out has another dtype than x")
-    s = [_strides(x, "x"), _strides(out, "out")] + ([_strides(x2, "x2"), _strides(out2, "out2")] if two else [])
-    p = [C.addressof(v) for v in s] + [None] * (4 - len(s))
-    with _on(x, stream):
-        _check("rq_rotary", lib().rq_rotary(
-            _dev(x), p[0], _dev(out), p[1], H, _dev(x2), p[2], _dev(out2), p[3], x2.shape[2] if two else 0,
-            _dtype_code(x), B, n, d, rot_dim, style, _dev(positions), positions.stride(0), f.ctypes.data, float(scale),
-            int(bool(inverse)), _stream(stream)))
+    _call("rq_rotary", x, stream, (
+        x.data_ptr(), _strides(x, "x"), out.data_ptr(), _strides(out, "out"), H, *p2, H2, _dtype_code(x), B, n, d,
+        rot_dim, style, positions.data_ptr(), ps[0], f.ctypes.data, scale, 1 if inverse else 0))
 
 
 def rq_evict_accumulate_workspace_bytes(G, n_q, T) -> int:
@@ -356,32 +381,28 @@ def rq_evict_accumulate_workspace_bytes(G, n_q, T) -> int:
 
 def rq_evict_accumulate(scores, G, n_q, T, softmax_scale, decay, acc, out, workspace, row_len=None, stream=None):
     """out [G][T] = decay * acc + sum over queries of softmax(softmax_scale * scores [G][n_q][T])."""
-    with _on(out, stream):
-        _check("rq_evict_accumulate", lib().rq_evict_accumulate(
-            _dev(scores), G, n_q, T, _dev(row_len), float(softmax_scale), float(decay), _dev(acc), _dev(out),
-            _dev(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _stream(stream)))
+    _call("rq_evict_accumulate", out, stream, (
+        _ptr(scores), G, n_q, T, _ptr(row_len), softmax_scale, decay, _ptr(acc), out.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size()))
 
 
 def rq_evict_select(acc, G, T, keep, idx, count, length=None, n_sink=0, n_recent=0, stream=None):
     """idx int32 [G][keep]: the tokens to keep of each group, ascending, then -1; count int32 [G]."""
-    with _on(idx, stream):
-        _check("rq_evict_select", lib().rq_evict_select(_dev(acc), G, T, _dev(length), keep, n_sink, n_recent,
-                                                        _dev(idx), _dev(count), _stream(stream)))
+    _call("rq_evict_select", idx, stream, (_ptr(acc), G, T, _ptr(length), keep, n_sink, n_recent, idx.data_ptr(),
+                                           count.data_ptr()))
 
 
 def rq_evict_gather(idx, count, G, keep, T, arrays, T_dst=None, stream=None):
     """Move the records idx [G][keep] of every (src [G][T]..., dst [G][T_dst]...) pair of contiguous tensors."""
-    rows = (Rows * len(arrays))()
     T_dst = keep if T_dst is None else T_dst
-    for r, (src, dst) in zip(rows, arrays):
-        r.src, r.dst = src.data_ptr(), dst.data_ptr()
-        r.row_bytes = src.numel() * src.element_size() // max(1, G * T)
-        if dst.numel() * dst.element_size() != r.row_bytes * G * T_dst:
+    rows = []
+    for src, dst in arrays:
+        size = src.numel() * src.element_size() // max(1, G * T)
+        if dst.numel() * dst.element_size() != size * G * T_dst:
             raise ValueError("rq_evict_gather: dst does not hold [G][T_dst] records of src's size")
-    with _on(idx, stream):
-        _check("rq_evict_gather", lib().rq_evict_gather(_dev(idx), _dev(count), G, keep, T, T_dst, C.addressof(rows),
-                                                        len(arrays), _stream(stream)))
+        rows += (src.data_ptr(), dst.data_ptr(), size)
+    _call("rq_evict_gather", idx, stream, (idx.data_ptr(), count.data_ptr(), G, keep, T, T_dst,
+                                           struct.pack(f"{len(rows)}q", *rows), len(arrays)))
 
 
 def qjl_tree_attention_workspace_bytes(B, n_kv_heads, n_rep, n_nodes, d, m, T) -> int:
@@ -395,27 +416,27 @@ def qjl_tree_attention(q, k_new, v_new, tree_mask, m, proj, signs, sk_norms, T, 
     """Attention of drafted tokens q [B, n_nodes, heads, d] over the compressed cache and over k_new, v_new
     [B, n_nodes, kv_heads, d]; tree_mask int64 [B or 1, n_nodes, words] (None: a chain); out bf16 of q's shape."""
     import torch
-    B, n, H, d = q.shape
-    kv = k_new.shape[2]
-    if tuple(k_new.shape) != (B, n, kv, d) or v_new.shape != k_new.shape or out.shape != q.shape or kv < 1 or H % kv:
+    shape, kshape = q.shape, k_new.shape
+    B, n, H, d = shape
+    kv = kshape[2]
+    if kshape != (B, n, kv, d) or v_new.shape != kshape or out.shape != shape or kv < 1 or H % kv:
         raise ValueError("qjl_tree_attention: k_new, v_new [B, n_nodes, kv_heads, d] and out of q's shape expected")
-    if any(t.dtype != torch.bfloat16 for t in (q, k_new, v_new, out)):
+    bf16 = torch.bfloat16
+    if q.dtype != bf16 or k_new.dtype != bf16 or v_new.dtype != bf16 or out.dtype != bf16:
         raise TypeError("qjl_tree_attention: bfloat16 q, k_new, v_new and out expected")
     stride = 0
     if tree_mask is not None:
-        if tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, B) or \
-                tuple(tree_mask.shape[1:]) != (n, (n + 63) // 64) or tree_mask.element_size() != 8 or \
-                not tree_mask.is_contiguous():
+        ms = tree_mask.shape
+        if len(ms) != 3 or ms[0] not in (1, B) or ms[1] != n or ms[2] != (n + 63) // 64 or \
+                tree_mask.element_size() != 8 or not tree_mask.is_contiguous():
             raise ValueError("qjl_tree_attention: contiguous 64-bit tree_mask [B or 1, n_nodes, ceil(n_nodes / 64)] expected")
-        stride = tree_mask.stride(0) if tree_mask.shape[0] > 1 else 0
-    s = [_strides(t, w) for t, w in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (out, "out"))]
-    p = [C.addressof(v) for v in s]
-    c = None if centroids is None else np.ascontiguousarray(np.asarray(centroids, dtype=np.float32))
-    vc = np.ascontiguousarray(np.asarray(v_centroids, dtype=np.float32))
-    with _on(q, stream):
-        _check("qjl_tree_attention", lib().qjl_tree_attention(
-            _dev(q), p[0], _dev(k_new), p[1], _dev(v_new), p[2], B, kv, H // kv, n, d, _dev(tree_mask), stride, m,
-            _dev(proj), _dtype_code(proj), _dev(signs), _dev(sk_norms), T, _dev(kv_len), _dev(codes), _dev(norms), bits,
-            layout, int(use_signs), sign_seed, None if c is None else c.ctypes.data, _dev(v_codes), _dev(v_norms), v_bits,
-            v_layout, int(v_use_signs), v_sign_seed, vc.ctypes.data, float(softmax_scale), _dev(out), p[3],
-            _dev(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        stride = n * ms[2] if ms[0] > 1 else 0
+    c = None if centroids is None else _host(centroids, np.float32)
+    vc = _host(v_centroids, np.float32)
+    _call("qjl_tree_attention", q, stream, (
+        q.data_ptr(), _strides(q, "q"), k_new.data_ptr(), _strides(k_new, "k_new"), v_new.data_ptr(),
+        _strides(v_new, "v_new"), B, kv, H // kv, n, d, _ptr(tree_mask), stride, m, proj.data_ptr(), _dtype_code(proj),
+        _ptr(signs), _ptr(sk_norms), T, _ptr(kv_len), _ptr(codes), _ptr(norms), bits, layout, int(use_signs),
+        sign_seed, None if c is None else c.ctypes.data, _ptr(v_codes), _ptr(v_norms), v_bits, v_layout,
+        int(v_use_signs), v_sign_seed, vc.ctypes.data, softmax_scale, out.data_ptr(), _strides(out, "out"),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size()))

@@ -21,8 +21,8 @@
 //                        shared memory, whose bandwidth bounds this kernel otherwise.  Then half the token's values,
 //                        V' = fp16(c) * fp16(n / d), to shared memory.
 //   MMA 1 (one thread)   S^T[token][row] += K slice (TMEM) . Q^T slice (shared memory).
-//   softmax (8 warps)    thread = token and half of the rows: p = 2^(s g cq + (8 - ref)), fp16 P to shared memory.  The
-//                        reference `ref` of a row is the maximum of the segment's first tile and moves only when a
+//   softmax (4 or 8 warps) thread = token, rows in chunks of 32: p = 2^(s g cq + (8 - ref)), fp16 P to shared memory.
+//                        The reference `ref` of a row is the maximum of the segment's first tile and moves only when a
 //                        score passes it by 7 (2^15 is the most fp16 weights take): the usual tile needs one vote
 //                        and no reduction over tokens.
 //   MMA 2 (one thread)   O^T[d][row] += V'^T . P, accumulated in TMEM over the segment.
@@ -35,21 +35,34 @@ namespace rq {
 
 constexpr int kTrTok = 128;                       // tokens a tile (M of both products' token side)
 constexpr int kTrD = 128;
-constexpr int kTrThreads = 18 * 32;
 constexpr int kTrVBytes = kTrTok * kTrD * 2;      // one value tile, fp16
 constexpr float kTrShift = 8.0f;                  // weight of the reference: 2^8
 constexpr float kTrMost = 15.0f;                  // largest exponent an fp16 weight may have
 
-__host__ __device__ inline int tr_kslots(int nb) { return nb == 128 ? 4 : 8; }
+constexpr int kTrAhead = 4;                       // tiles that the cache's records are prefetched into L2 ahead
+
+// Warps of a CTA: NB / 32 groups of four softmax warps (a group has 32 rows), two groups of four producer warps (a
+// group unpacks every second tile), two issuing warps.
+__host__ __device__ constexpr int tr_softmax_warps(int nb) { return nb / 8; }
+__host__ __device__ constexpr int tr_producer_groups(int) { return 2; }
+__host__ __device__ constexpr int tr_threads(int nb) { return (tr_softmax_warps(nb) + 4 * tr_producer_groups(nb) + 2) * 32; }
+__host__ __device__ constexpr int tr_ctas(int nb) { return nb == 32 ? 2 : 1; }
+// TMEM: score buffers, O, the weight sums (16 columns), key slots of 32 columns
+__host__ __device__ constexpr int tr_sbufs(int nb) { return nb == 128 ? 1 : 2; }
+__host__ __device__ constexpr int tr_kslots(int nb) { return nb == 32 ? 4 : nb == 64 ? 8 : 6; }
+__host__ __device__ constexpr int tr_tmem(int nb) { return nb == 32 ? 256 : 512; }
+// log2 of the copies of the value and key lookup tables (more copies: fewer bank conflicts)
+__host__ __device__ constexpr int tr_vcl(int nb) { return nb == 32 ? 3 : 4; }
+__host__ __device__ constexpr int tr_kcl(int nb) { return nb == 64 ? 4 : 3; }
 __host__ __device__ inline size_t tr_pbytes(int nb) { return (size_t)(nb > 64 ? 2 : 1) * kTrTok * 128; }
-__host__ __device__ inline size_t tr_lut_bytes(int pw, int copies)
+__host__ __device__ inline size_t tr_lut_bytes(int pw, int cl)
 {
-    return pw == 0 ? 0 : pw <= 4 ? ((size_t)1 << (2 * pw)) * copies * 4 : ((size_t)256 * copies * 2);
+    return pw == 0 ? 0 : pw <= 4 ? ((size_t)4 << (2 * pw + cl)) : ((size_t)512 << cl);
 }
-__host__ __device__ inline size_t tr_smem(int nb, int kb, int pw, int vpw, int np, int copies)
+__host__ __device__ inline size_t tr_smem(int nb, int kb, int pw, int vpw, int np, int nv)
 {
-    return 1024 + (size_t)nb * kb * 2 + 2 * kTrVBytes + np * tr_pbytes(nb) + tr_lut_bytes(pw, copies) +
-           tr_lut_bytes(vpw, copies) + (size_t)nb * 12 + (size_t)4 * nb * 4 + 8 * 40 + 16;
+    return 1024 + (size_t)nb * kb * 2 + nv * kTrVBytes + np * tr_pbytes(nb) + tr_lut_bytes(pw, tr_kcl(nb)) +
+           tr_lut_bytes(vpw, tr_vcl(nb)) + 2048 + (size_t)nb * 12 + (size_t)5 * nb * 4 + 8 * 40 + 48;
 }
 // Partial result of one (CTA, row block) segment: O [nb][128], m [nb], l [nb].
 __host__ __device__ inline size_t tr_part_floats(int nb) { return (size_t)nb * (kTrD + 2); }
@@ -61,28 +74,68 @@ __device__ __forceinline__ float tr_ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
+{
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
+// The three kernels are launched so that each may start while the one before it runs: what does not depend on it comes
+// before tr_wait_previous.
+__device__ __forceinline__ void tr_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void tr_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Shared memory by 32-bit address (a lookup in a table that nothing writes any more; and accesses in program order).
+__device__ __forceinline__ uint32_t tr_lds(uint32_t addr)
+{
+    uint32_t r;
+    asm("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ uint32_t tr_lds16(uint32_t addr)
+{
+    uint16_t r;
+    asm("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ float4 tr_lds_f4(uint32_t addr)
+{
+    float4 r;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ void tr_sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 __device__ __forceinline__ void tr_bar(int id)
 {
     asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
 
-__device__ __forceinline__ bool tr_bar_or(int id, bool p)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(p ? 1u : 0u), "r"(id)
-        : "memory");
-    return r != 0;
-}
-
 __device__ __forceinline__ void tr_arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// True in one lane of a converged warp.  (Measured: products issued under `lane == 0` cost the issuing thread about 200
+// cycles each, since their descriptors are then not warp-uniform to the compiler; under the elected lane they do not.)
+__device__ __forceinline__ bool tr_elect()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], kind::f16.
@@ -96,25 +149,25 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uin
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+        "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31]), "r"(taddr)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+// Fetch [p, p + bytes) into L2 (both rounded down to 16 bytes).
+__device__ __forceinline__ void tr_prefetch(const void *p, int64_t bytes)
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
-        "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-        "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-        : "memory");
+    const uint64_t a = reinterpret_cast<uint64_t>(p) & ~15ull;
+    const uint32_t n = (uint32_t)((reinterpret_cast<uint64_t>(p) + bytes - a) & ~15ull);
+    if (n) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -130,22 +183,20 @@ __device__ __forceinline__ uint64_t tr_sdesc(uint32_t saddr, uint32_t lbo, uint3
     return d;
 }
 
-// Reduce v[0 .. N) over the 32 lanes of a warp (N = 32 or 16): lane l returns the result of column l % N.
-template <int N, typename Op>
-__device__ __forceinline__ float tr_reduce_columns(float *v, int lane, Op op)
+// Reduce v[0 .. 32) over the 32 lanes of a warp: lane l returns the result of column l.
+template <typename Op>
+__device__ __forceinline__ float tr_reduce_columns(uint32_t *v, int lane, Op op)
 {
 #pragma unroll
-    for (int o = N / 2; o >= 1; o >>= 1) {
+    for (int o = 16; o >= 1; o >>= 1) {
         const bool up = lane & o;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
-            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            const uint32_t send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = __float_as_uint(op(__uint_as_float(keep), __uint_as_float(__shfl_xor_sync(0xffffffffu, send, o))));
         }
     }
-    float x = v[0];
-    if (N == 16) x = op(x, __shfl_xor_sync(0xffffffffu, x, 16));
-    return x;
+    return __uint_as_float(v[0]);
 }
 
 __device__ __forceinline__ int64_t tr_len(const TreeArgs &a, int64_t g)
@@ -155,82 +206,127 @@ __device__ __forceinline__ int64_t tr_len(const TreeArgs &a, int64_t g)
     return n < 0 ? 0 : (n < a.T ? n : a.T);
 }
 
-// Position in the list of (group, row block, tile) items: group g's items are [off[g] rb_count, off[g+1] rb_count).
+// Position in the list of (group, row block, tile) items: group g's items are [off[g] rbs, off[g + 1] rbs).
 struct TreeIter {
-    int64_t g, n, tile;
-    int rb;
-    __device__ void seek(const int64_t *off, int64_t G, int rbs, int64_t it)
+    int64_t g, row;                               // row: cache row of the tile's first token
+    int rb, tile, n, left;                        // left: the group's tokens from the tile's first on
+    __device__ void group(const TreeArgs &a)
     {
-        int64_t lo = 0, hi = G;                   // off[lo] rbs <= it < off[hi] rbs
+        n = (int)(a.off[g + 1] - a.off[g]);
+    }
+    __device__ void place(const TreeArgs &a)
+    {
+        row = g * a.T + (int64_t)tile * kTrTok;
+        left = (int)(tr_len(a, g) - (int64_t)tile * kTrTok < 0x7fffffff ? tr_len(a, g) - (int64_t)tile * kTrTok : 0x7fffffff);
+    }
+    __device__ void seek(const TreeArgs &a, int64_t it)
+    {
+        int64_t lo = 0, hi = a.G;                 // off[lo] rbs <= it < off[hi] rbs
         while (hi - lo > 1) {
             const int64_t mid = (lo + hi) >> 1;
-            if (off[mid] * rbs <= it) lo = mid; else hi = mid;
+            if (a.off[mid] * a.rbs <= it) lo = mid; else hi = mid;
         }
         g = lo;
-        n = off[g + 1] - off[g];
-        const int64_t rest = it - off[g] * rbs;
+        group(a);
+        const int64_t rest = it - a.off[g] * a.rbs;
         rb = (int)(rest / n);
-        tile = rest - rb * n;
+        tile = (int)(rest - (int64_t)rb * n);
+        place(a);
     }
     // advance by one item (the caller knows that there is one); true when the row block changes
-    __device__ bool next(const int64_t *off, int rbs)
+    __device__ bool next(const TreeArgs &a)
     {
-        if (++tile < n) return false;
+        if (++tile < n) {
+            row += kTrTok;
+            left -= kTrTok;
+            return false;
+        }
         tile = 0;
-        if (++rb == rbs) {
+        if (++rb == a.rbs) {
             rb = 0;
             do {
                 ++g;
-                n = off[g + 1] - off[g];
+                group(a);
             } while (n == 0);
         }
+        place(a);
         return true;
     }
 };
 
-// 32 sign bits to fp16 +-mag, 16 pairs.  Pair i is (bit i, bit i + 16): one shift and one masked or; the score
-// product sums over all of them, so the query operand has its coordinates in the same order (tr_sign_column).
+// 32 sign bits to 16 pairs of fp16; pair i is (bit i, bit i + 16) in both forms.  The score product sums over all
+// of them, so the query operand has its coordinates in the same order (tr_sign_column).
+// +-mag: one shift and one masked or a pair.
 __device__ __forceinline__ void tr_signs(uint32_t w, uint32_t mag2, uint32_t *o)
 {
     const uint32_t n = ~w;
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = mag2 | ((n << (15 - i)) & 0x80008000u);
 }
+// The bits where they lie: a set bit p (5 .. 12) of an fp16 value alone is the number c_p = 2^-19 ... 2^-11 (up to
+// p = 9 a subnormal one), so a pair costs one mask, and sign = 2 bit - 1 with c_p taken into the query operand:
+// sum_i sign_i q_i = 2^19 sum_i (bit_i c_p) (2^-18 q_i / c_p) - sum_i q_i.
+__device__ __forceinline__ void tr_bits(uint32_t w, uint32_t *o)
+{
+    const uint32_t lo = w << 5, hi = w >> 3;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        o[i] = lo & (0x00200020u << i);
+        o[8 + i] = hi & (0x00200020u << i);
+    }
+}
+constexpr float kTrBitScale = 0x1p19f;
+// 2^-18 / c_p of sketch coordinate i
+__host__ __device__ inline float tr_bit_factor(int i)
+{
+    const int p = 5 + (i & 7);                    // c_p = 2^(p - 24) below 10, then 2^-14, 2^-13, 2^-11
+    return p < 10 ? (float)(1 << (10 - p)) * 0.0625f : p == 10 ? 0.0625f : p == 11 ? 0.03125f : 0.0078125f;
+}
 // Column, in its 64-column slice, of sketch coordinate i (0 .. 63).
 __host__ __device__ inline int tr_sign_column(int i) { return (i & 32) | ((i & 15) << 1) | ((i >> 4) & 1); }
 
-// 64 codes of PW bits (kc) to 32 pairs of fp16 centroids.
-template <int PW>
-__device__ __forceinline__ void tr_lookup(const uint32_t *kc, const uint32_t *lut, int copies_log2, uint32_t lane_copy, uint32_t *o)
+// Pairs [FROM, FROM + N) of 64 codes of PW bits to fp16 centroids: the pair's 2 PW bits index a table of pairs in 2^CL
+// copies.
+template <int PW, int CL, int FROM, int N>
+__device__ __forceinline__ void tr_lookup(const uint32_t *kc, uint32_t lut, uint32_t lane4, uint32_t *out)
 {
+    uint32_t *o = out - FROM;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = FROM; i < FROM + N; ++i) {
         if constexpr (PW <= 4) {
-            o[i] = lut[(unpack_code<32, 2 * PW>(kc, i) << copies_log2) + lane_copy];
+            constexpr int B = 2 * PW;
+            constexpr uint32_t mask = ((1u << B) - 1u) << (CL + 2);
+            const int bit = i * B, w = bit >> 5, sh = (bit & 31) - (CL + 2);
+            uint32_t x;
+            if ((bit & 31) + B > 32) x = __funnelshift_r(kc[w], kc[w + 1 < 16 ? w + 1 : w], bit & 31) << (CL + 2);
+            else x = sh >= 0 ? kc[w] >> (sh >= 0 ? sh : 0) : kc[w] << (sh < 0 ? -sh : 0);
+            o[i] = tr_lds(lut + ((x & mask) | lane4));
         } else {
+            const uint32_t l16 = lut + (lane4 >> 1);
             const uint32_t ca = unpack_code<64, PW>(kc, 2 * i), cb = unpack_code<64, PW>(kc, 2 * i + 1);
-            const uint16_t *l16 = reinterpret_cast<const uint16_t *>(lut);
-            o[i] = (uint32_t)l16[(ca << copies_log2) + lane_copy] | ((uint32_t)l16[(cb << copies_log2) + lane_copy] << 16);
+            o[i] = tr_lds16(l16 + (ca << (CL + 1))) | (tr_lds16(l16 + (cb << (CL + 1))) << 16);
         }
     }
 }
 
-__device__ __forceinline__ void tr_lookup_any(int pw, const uint32_t *kc, const uint32_t *lut, int cl, uint32_t lc, uint32_t *o)
+template <int CL, int FROM, int N>
+__device__ __forceinline__ void tr_lookup_any(int pw, const uint32_t *kc, uint32_t lut, uint32_t lane4, uint32_t *o)
 {
     switch (pw) {
-    case 1: tr_lookup<1>(kc, lut, cl, lc, o); break;
-    case 2: tr_lookup<2>(kc, lut, cl, lc, o); break;
-    case 3: tr_lookup<3>(kc, lut, cl, lc, o); break;
-    case 4: tr_lookup<4>(kc, lut, cl, lc, o); break;
-    default: tr_lookup<8>(kc, lut, cl, lc, o); break;
+    case 1: tr_lookup<1, CL, FROM, N>(kc, lut, lane4, o); break;
+    case 2: tr_lookup<2, CL, FROM, N>(kc, lut, lane4, o); break;
+    case 3: tr_lookup<3, CL, FROM, N>(kc, lut, lane4, o); break;
+    case 4: tr_lookup<4, CL, FROM, N>(kc, lut, lane4, o); break;
+    default: tr_lookup<8, CL, FROM, N>(kc, lut, lane4, o); break;
     }
 }
 
-// 8 pw bytes (64 codes) at p, 8-byte aligned.
+// Words [2 from, 2 to) of the 8 pw bytes (64 codes) at p, 8-byte aligned.
+template <int FROM, int TO>
 __device__ __forceinline__ void tr_load_codes(const uint8_t *p, int pw, bool valid, uint32_t *w)
 {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = FROM; q < TO; ++q) {
         uint2 v = make_uint2(0u, 0u);
         if (q < pw && valid) v = __ldg(reinterpret_cast<const uint2 *>(p) + q);
         w[2 * q] = v.x;
@@ -238,124 +334,140 @@ __device__ __forceinline__ void tr_load_codes(const uint8_t *p, int pw, bool val
     }
 }
 
-template <int NB>
-__global__ void __launch_bounds__(kTrThreads, 1)
+template <int NB, bool TWO>
+__global__ void __launch_bounds__(tr_threads(NB), tr_ctas(NB))
 tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ QuantTables TK,
-                      const __grid_constant__ QuantTables TV, int np, int copies_log2)
+                      const __grid_constant__ QuantTables TV, int np, int nv)
 {
-    constexpr int CW = NB / 2, CH = CW < 32 ? CW : 32, NCH = CW / CH;
-    constexpr int KS = NB == 128 ? 4 : 8;         // key slots in TMEM
-    const bool two = a.pw != 0;
-    const int kb = a.kb, nsl = kb / 64, dsl = two ? 2 : 0;
+    constexpr int SW = tr_softmax_warps(NB), NPG = tr_producer_groups(NB), PW = 4 * NPG;
+    constexpr int VCL = tr_vcl(NB), KCL = tr_kcl(NB), threads = tr_threads(NB), KS = tr_kslots(NB), NS = tr_sbufs(NB);
+    // Every producer group has its own key slots: it may be tiles ahead of the products, but then never more than one
+    // phase ahead of a slot's barrier, which is what a parity can tell.
+    constexpr int SPG = KS / NPG;
+    const int kb = a.kb, nsl = kb / 64, dsl = TWO ? 2 : 0;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = base;
     uint8_t *sV = sQ + (size_t)NB * kb * 2;
-    uint8_t *sP = sV + 2 * kTrVBytes;
-    uint32_t *klut = reinterpret_cast<uint32_t *>(sP + np * tr_pbytes(NB));
-    uint32_t *vlut = klut + tr_lut_bytes(a.pw, 1 << copies_log2) / 4;
-    float *sF = reinterpret_cast<float *>(vlut + tr_lut_bytes(a.vpw, 1 << copies_log2) / 4);   // per pair of rows: cq, cq, 8 - ref, 8 - ref
-    float *sAl = sF + 2 * NB;                     // [NB] rescale factors
-    float *sX = sAl + NB;                         // [4][NB] column reductions by lane quarter
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(sX + 4 * NB);
+    uint8_t *sP = sV + (size_t)nv * kTrVBytes;
+    uint8_t *ones = sP + np * tr_pbytes(NB);      // 2 KB of fp16 ones: the sums' second operand
+    uint8_t *klut = ones + 2048;
+    uint8_t *vlut = klut + tr_lut_bytes(a.pw, KCL);
+    // per pair of rows: the operand's sums (-Q, -Q, pure sketch keys only), 8 - ref, 8 - ref
+    float4 *sF = reinterpret_cast<float4 *>(vlut + tr_lut_bytes(a.vpw, VCL));
+    float *sAl = reinterpret_cast<float *>(sF + NB / 2);                         // [NB] rescale factors
+    float *sX = sAl + NB;                         // [4][NB] column reductions by lane quarter, [NB] moves of the exponents
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(sX + 5 * NB);
     uint64_t *k_empty = k_full + KS;
     uint64_t *v_full = k_empty + KS;              // [2]
     uint64_t *s_full = v_full + 2;                // [2]
     uint64_t *s_empty = s_full + 2;               // [2]
     uint64_t *p_full = s_empty + 2;               // [2]
-    uint64_t *pv_done = p_full + 2;               // [2] by tile parity: P, V free, O holds the tile
-    uint64_t *o_empty = pv_done + 2;
+    uint64_t *pv_done = p_full + 2;               // [4] by tile modulo 4: P, V free, O holds the tile
+    uint64_t *o_empty = pv_done + 4;
     uint64_t *q_full = o_empty + 1;
     uint64_t *q_done = q_full + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_done + 1);
+    uint64_t *vote = q_done + 1;                  // [4] by softmax group
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(vote + 4);
+    volatile uint32_t *flag = tmem_slot + 1;      // [4][2] by softmax group and use parity
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t quarter = (uint32_t)(warp & 3);
-    const int copies = 1 << copies_log2;
-    auto fill = [&](const QuantTables &T, uint32_t *lut, int pw) {
+    tr_launch_next();
+    auto fill = [&](const QuantTables &T, uint8_t *dst, int pw, int cl) {
         if (pw == 0) return;
         if (pw <= 4) {
-            for (int i = tid; i < (1 << (2 * pw)) * copies; i += kTrThreads) {
-                const int e = i >> copies_log2, ca = e & ((1 << pw) - 1), cb = e >> pw;
+            uint32_t *lut = reinterpret_cast<uint32_t *>(dst);
+            for (int i = tid; i < 1 << (2 * pw + cl); i += threads) {
+                const int e = i >> cl, ca = e & ((1 << pw) - 1), cb = e >> pw;
                 const float fa = ca < T.levels ? T.centroid[ca] : 0.0f, fb = cb < T.levels ? T.centroid[cb] : 0.0f;
                 lut[i] = (uint32_t)__half_as_ushort(__float2half_rn(fa)) |
                          ((uint32_t)__half_as_ushort(__float2half_rn(fb)) << 16);
             }
         } else {
-            uint16_t *l16 = reinterpret_cast<uint16_t *>(lut);
-            for (int i = tid; i < 256 * copies; i += kTrThreads) {
-                const int e = i >> copies_log2;
+            uint16_t *l16 = reinterpret_cast<uint16_t *>(dst);
+            for (int i = tid; i < 256 << cl; i += threads) {
+                const int e = i >> cl;
                 l16[i] = __half_as_ushort(__float2half_rn(e < T.levels ? T.centroid[e] : 0.0f));
             }
         }
     };
-    fill(TK, klut, a.pw);
-    fill(TV, vlut, a.vpw);
+    if (TWO) fill(TK, klut, a.pw, KCL);
+    fill(TV, vlut, a.vpw, VCL);
+    for (int i = tid; i < 512; i += threads) reinterpret_cast<uint32_t *>(ones)[i] = 0x3C003C00u;
+    fence_proxy_async_smem();
     if (tid == 0) {
+        for (int b = 0; b < 8; ++b) flag[b] = 0u;
+        for (int b = 0; b < 4; ++b) mbar_init(&vote[b], 4);
         for (int b = 0; b < KS; ++b) { mbar_init(&k_full[b], 4); mbar_init(&k_empty[b], 1); }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&v_full[b], 8);
-            mbar_init(&s_full[b], 1); mbar_init(&s_empty[b], 8);
-            mbar_init(&p_full[b], 8); mbar_init(&pv_done[b], 1);
+            mbar_init(&v_full[b], 4);
+            mbar_init(&s_full[b], 1); mbar_init(&s_empty[b], SW);
+            mbar_init(&p_full[b], SW);
         }
-        mbar_init(o_empty, 8);
+        for (int b = 0; b < 4; ++b) mbar_init(&pv_done[b], 1);
+        mbar_init(o_empty, SW);
         mbar_init(q_full, 1);
         mbar_init(q_done, 1);
         fence_barrier_init();
     }
-    if (warp == 16) tmem_alloc(tmem_slot, 512);
+    if (warp == SW + PW) tmem_alloc(tmem_slot, tr_tmem(NB));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tS = tmem, tO = tmem + 2 * NB, tK = tmem + 3 * NB;
+    const uint32_t tS = tmem, tO = tmem + NS * NB, tL = tO + NB, tK = tL + 16;
 
-    const int64_t total = a.off[a.G] * a.rbs;
-    const int64_t it0 = total * blockIdx.x / gridDim.x, it1 = total * (blockIdx.x + 1) / gridDim.x;
-    const int64_t count = it1 - it0;
+    tr_wait_previous();
+    // the items are split over as many CTAs as have one
+    const int64_t total = a.off[a.G] * a.rbs, ctas = total < gridDim.x ? total : gridDim.x;
+    const int64_t it0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
+    const int count = blockIdx.x < ctas ? (int)(total * (blockIdx.x + 1) / ctas - it0) : 0;
     bool ok = true;
+    auto pv_wait = [&](int tile) { return mbar_wait(&pv_done[tile & 3], (uint32_t)((tile >> 2) & 1)); };
     TreeIter it;
-    if (count > 0) it.seek(a.off, a.G, a.rbs, it0);
+    if (count > 0) it.seek(a, it0);
 
-    if (count > 0 && warp >= 8 && warp < 16) {
+    if (count > 0 && warp >= SW && warp < SW + PW) {
         // ------------------------------------------------------------ producers
-        const int half = (warp - 8) >> 2;
+        const int group = (warp - SW) >> 2;
         const int r = (int)quarter * 32 + lane;                 // token of the tile
         const uint32_t sbytes = (uint32_t)a.m / 8, cbytes = 16u * a.pw, vbytes = 16u * a.vpw;
         const float kq = 1.2533141373155002512f / (float)a.m;
-        const uint32_t lc = (uint32_t)lane & (uint32_t)(copies - 1);
+        const uint32_t lane4k = 4u * ((uint32_t)lane & ((1u << KCL) - 1u)), lane4v = 4u * ((uint32_t)lane & ((1u << VCL) - 1u));
+        const uint32_t klut0 = smem_u32(klut), vlut0 = smem_u32(vlut), sV0 = smem_u32(sV);
         const int nsig = nsl - dsl;
-        uint2 sg[4];                                            // sign slices half, half + 2, ... of the sketch
-        uint32_t kc[16], vc[16];
-        uint16_t hn = 0, hr = 0, hv = 0;                        // first-stage, sketch and value norm
-        auto load_keys = [&](const TreeIter &p) {
-            const int64_t t = p.tile * kTrTok + r, kt = p.g * a.T + t;
-            const bool valid = t < tr_len(a, p.g);
+        uint2 sg[4];                                            // four sign slices, loaded a tile ahead
+        uint16_t hn = 0, hr = 0;                                // first-stage and sketch norm
+        auto load_signs = [&](const TreeIter &p, int first) {
+            const uint2 *src = reinterpret_cast<const uint2 *>(a.signs + (p.row + r) * sbytes) + first;
+            const bool valid = r < p.left;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sg[i] = make_uint2(0u, 0u);
-                if (2 * i + half < nsig && valid)
-                    sg[i] = __ldg(reinterpret_cast<const uint2 *>(a.signs + kt * sbytes) + 2 * i + half);
-            }
-            if (two) {
-                tr_load_codes(a.codes + kt * cbytes + half * 8 * a.pw, a.pw, valid, kc);
-                hn = valid ? __ldg(a.norms + kt) : (uint16_t)0;
-                hr = valid ? __ldg(a.sk_norms + kt) : (uint16_t)0;
+                if (first + i < nsig && valid) sg[i] = __ldg(src + i);
             }
         };
-        auto load_values = [&](const TreeIter &p) {
-            const int64_t t = p.tile * kTrTok + r, kt = p.g * a.T + t;
-            const bool valid = t < tr_len(a, p.g);
-            tr_load_codes(a.vcodes + kt * vbytes + half * 8 * a.vpw, a.vpw, valid, vc);
-            hv = valid ? __ldg(a.vnorms + kt) : (uint16_t)0;
+        auto load_norms = [&](const TreeIter &p) {
+            if (TWO) {
+                hn = r < p.left ? __ldg(a.norms + p.row + r) : (uint16_t)0;
+                hr = r < p.left ? __ldg(a.sk_norms + p.row + r) : (uint16_t)0;
+            }
         };
-        load_keys(it);
-        load_values(it);
-        int64_t pos0 = 0;                                       // slices before this tile
-        for (int64_t c = 0; c < count && ok; ++c, pos0 += nsl) {
+        // this group's next tile, `c` counting the CTA's tiles
+        auto advance = [&](TreeIter &p, int c) {
+#pragma unroll 1
+            for (int i = 0; i < NPG && c + i + 1 < count; ++i) p.next(a);
+        };
+        for (int i = 0; i < group && i + 1 < count; ++i) it.next(a);
+        if (group < count) {
+            load_signs(it, 0);
+            load_norms(it);
+        }
+        for (int c = group; c < count && ok; c += NPG) {
             uint32_t rho2 = 0x3C003C00u;
-            if (two) {
+            if (TWO) {
                 // the sketch term scaled to share the first stage's accumulator and factor n / d
                 const float n1 = h16_to_f32(hn);
                 float rho = 0.0f;
@@ -363,75 +475,91 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                 const uint32_t h = (uint32_t)__half_as_ushort(__float2half_rn(rho));
                 rho2 = h | (h << 16);
             }
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {                       // slice 2 i + half: a code slice, or sign slice - dsl
-                const int s = 2 * i + half;
-                if (s >= nsl) break;
-                const int64_t pos = pos0 + s;
-                const int slot = (int)(pos % KS);
+            const bool valid = r < it.left;
+            const int64_t row = it.row + r;
+#pragma unroll 1
+            for (int s = 0; s < nsl; ++s) {                     // a code slice (the first two), or sign slice s - dsl
+                const uint32_t n = (uint32_t)(c / NPG * nsl + s);       // slices of this group before
+                const int slot = group * SPG + (int)(n % SPG);
                 uint32_t o[32];
-                if (two && i == 0) {
-                    tr_lookup_any(a.pw, kc, klut, copies_log2, lc, o);
+                if (TWO && s < 2) {
+                    uint32_t kc[16];
+                    tr_load_codes<0, 8>(a.codes + row * cbytes + s * 8 * a.pw, a.pw, valid, kc);
+                    tr_lookup_any<KCL, 0, 32>(a.pw, kc, klut0, lane4k, o);
                 } else {
-                    const int q = two ? i - 1 : i;
-                    uint2 w = make_uint2(0u, 0u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e == q) w = sg[e];
-                    tr_signs(w.x, rho2, o);
-                    tr_signs(w.y, rho2, o + 16);
+                    if (TWO) {
+                        tr_signs(sg[0].x, rho2, o);
+                        tr_signs(sg[0].y, rho2, o + 16);
+                    } else {
+                        tr_bits(sg[0].x, o);
+                        tr_bits(sg[0].y, o + 16);
+                    }
+                    sg[0] = sg[1];
+                    sg[1] = sg[2];
+                    sg[2] = sg[3];
+                    if (s - dsl == 3 && nsig > 4) load_signs(it, 4);
                 }
-                if (pos >= KS && ok && !mbar_wait(&k_empty[slot], (uint32_t)((pos / KS - 1) & 1))) ok = false;
+                if (n >= SPG && ok && !mbar_wait(&k_empty[slot], (n / SPG - 1) & 1)) ok = false;
                 tc_fence_after();
-                const uint32_t dst = tK + (uint32_t)slot * 32u + (quarter << 21);
-                tmem_st16(dst, o);
-                tmem_st16(dst + 16, o + 16);
+                tmem_st32(tK + (uint32_t)slot * 32u + (quarter << 21), o);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tr_arrive(&k_full[slot]);
             }
-            TreeIter nx = it;
-            const bool more = c + 1 < count;
-            if (more) {
-                nx.next(a.off, a.rbs);
-                load_keys(nx);
+            uint32_t vc[16];
+            const uint16_t hv = valid ? __ldg(a.vnorms + row) : (uint16_t)0;
+            tr_load_codes<0, 4>(a.vcodes + row * vbytes, a.vpw, valid, vc);
+            advance(it, c);
+            if (c + NPG < count) {
+                load_signs(it, 0);
+                load_norms(it);
             }
-            // half the value row: rows of tokens, two 64-wide atoms of d
-            uint32_t o[32];
-            tr_lookup_any(a.vpw, vc, vlut, copies_log2, lc, o);
+            // the value row: rows of tokens, two 64-wide atoms of d
             const float fv = __fmul_rn(h16_to_f32(hv), 1.0f / (float)kTrD);
             const __half2 f2 = __half2half2(__float2half_rn(fv));
-            const int vb = (int)(c & 1);
-            if (c >= 2 && ok && !mbar_wait(&pv_done[vb], (uint32_t)(((c >> 1) - 1) & 1))) ok = false;
-            uint8_t *Vr = sV + (size_t)vb * kTrVBytes + (size_t)half * (kTrVBytes / 2) + (size_t)(r >> 3) * 1024 + (size_t)(r & 7) * 128;
+            const int vb = nv == 2 ? c & 1 : 0;
+            uint32_t Vr = sV0 + (uint32_t)vb * kTrVBytes + (uint32_t)r * 128u;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half, Vr += kTrVBytes / 2) {
+                if (a.vpw > 4) tr_load_codes<4, 8>(a.vcodes + row * vbytes + half * 8 * a.vpw, a.vpw, valid, vc);
+                if (half == 0 && c >= nv && ok && !pv_wait(c - nv)) ok = false;  // the tile whose values lie here.  With a
+                // barrier for every fourth tile the phase before this one has been waited for (at this group's last
+                // tile) and the next one needs this tile's values, so the parity tells.
+                auto store = [&](int ch0, const uint32_t *o) {
 #pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-                uint32_t w[4];
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2 hv2 = __hmul2(*reinterpret_cast<const __half2 *>(&o[4 * ch + e]), f2);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&hv2);
-                }
-                *reinterpret_cast<uint4 *>(Vr + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const __half2 hv2 = __hmul2(*reinterpret_cast<const __half2 *>(&o[4 * ch + e]), f2);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&hv2);
+                        }
+                        tr_sts128(Vr + (uint32_t)(((ch0 + ch) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    }
+                };
+                uint32_t o[16];
+                tr_lookup_any<VCL, 0, 16>(a.vpw, vc, vlut0, lane4v, o);
+                store(0, o);
+                tr_lookup_any<VCL, 16, 16>(a.vpw, vc, vlut0, lane4v, o);
+                if (half == 0) tr_load_codes<0, 4>(a.vcodes + row * vbytes + 8 * a.vpw, a.vpw, valid, vc);
+                store(4, o);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tr_arrive(&v_full[vb]);
-            if (more) load_values(nx);
-            it = nx;
+            if (lane == 0) tr_arrive(&v_full[c & 1]);
         }
-    } else if (count > 0 && warp == 16) {
+    } else if (count > 0 && warp == SW + PW) {
         // ------------------------------------------------------------ MMA 1: S^T = K . Q^T
         const uint32_t sQ0 = smem_u32(sQ);
         const uint32_t idesc = idesc_f16(false, kTrTok, NB);
         const uint32_t qbytes = (uint32_t)NB * kb * 2;
         bool fresh = true;
-        int64_t seg = 0, pos = 0;
-        for (int64_t c = 0; c < count && ok; ++c) {
+        int seg = 0;
+        for (int c = 0; c < count && ok; ++c) {
             if (fresh) {
                 if (seg > 0) {
-                    if (lane == 0) mma_commit(q_done);
+                    if (tr_elect()) mma_commit(q_done);
                     if (!mbar_wait(q_done, (uint32_t)((seg - 1) & 1))) { ok = false; break; }
                 }
                 if (lane == 0) {
@@ -441,258 +569,231 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                 if (!mbar_wait(q_full, (uint32_t)(seg & 1))) { ok = false; break; }
                 ++seg;
             }
-            const int sb = (int)(c & 1);
-            if (c >= 2 && !mbar_wait(&s_empty[sb], (uint32_t)(((c >> 1) - 1) & 1))) { ok = false; break; }
+            const int before = c - NS;                          // the tile whose scores lie in the buffer
+            if (before >= 0 && !mbar_wait(&s_empty[before & 1], (uint32_t)((before >> 1) & 1))) { ok = false; break; }
             tc_fence_after();
-            for (int s = 0; s < nsl; ++s, ++pos) {
-                const int slot = (int)(pos % KS);
-                if (!mbar_wait(&k_full[slot], (uint32_t)((pos / KS) & 1))) { ok = false; break; }
+            for (int s = 0; s < nsl; ++s) {
+                const uint32_t n = (uint32_t)(c / NPG * nsl + s);
+                const int slot = c % NPG * SPG + (int)(n % SPG);
+                if (!mbar_wait(&k_full[slot], (n / SPG) & 1)) { ok = false; break; }
                 tc_fence_after();
-                if (lane == 0) {
+                if (tr_elect()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16_ta(tS + (uint32_t)sb * NB, tK + (uint32_t)slot * 32u + kk * 8u,
+                        mma_f16_ta(tS + (uint32_t)(c % NS) * NB, tK + (uint32_t)slot * 32u + kk * 8u,
                                    sdesc_k_sw128(sQ0 + (uint32_t)s * (NB * 128u) + kk * 32u), idesc,
                                    (s > 0 || kk > 0) ? 1u : 0u);
                     mma_commit(&k_empty[slot]);
-                    if (s == nsl - 1) mma_commit(&s_full[sb]);
+                    if (s == nsl - 1) mma_commit(&s_full[c & 1]);
                 }
                 __syncwarp();
             }
-            if (c + 1 < count) fresh = it.next(a.off, a.rbs);
+            if (c + 1 < count) fresh = it.next(a);
         }
         if (seg > 0) {                                          // all products done before TMEM is freed
-            if (lane == 0) mma_commit(q_done);
+            if (tr_elect()) mma_commit(q_done);
             if (ok) mbar_wait(q_done, (uint32_t)((seg - 1) & 1));
         }
-    } else if (count > 0 && warp == 17) {
-        // ------------------------------------------------------------ MMA 2: O^T += V'^T . P
-        const uint32_t sP0 = smem_u32(sP), sV0 = smem_u32(sV);
+    } else if (count > 0 && warp == SW + PW + 1) {
+        // ------------------------------------------------------------ MMA 2: O^T += V'^T . P; L2 prefetch
+        const uint32_t sP0 = smem_u32(sP), sV0 = smem_u32(sV), ones0 = smem_u32(ones);
         const uint32_t idesc = idesc_f16(false, kTrD, NB) | (1u << 15) | (1u << 16);    // both operands MN-major
         bool fresh = true;
-        int64_t seg = 0;
-        for (int64_t c = 0; c < count && ok; ++c) {
-            const int b = (int)(c & 1), pb = np == 2 ? b : 0;
+        int seg = 0;
+        TreeIter pf = it;
+        int npf = 0;
+        auto fetch = [&]() {                                    // one tile of records
+            const int64_t n = pf.left < kTrTok ? pf.left : kTrTok;
+            if (lane == 0) {
+                tr_prefetch(a.signs + pf.row * (a.m / 8), n * (a.m / 8));
+                tr_prefetch(a.vcodes + pf.row * (16 * a.vpw), n * (16 * a.vpw));
+                tr_prefetch(a.sk_norms + pf.row, n * 2);
+                tr_prefetch(a.vnorms + pf.row, n * 2);
+                if (TWO) {
+                    tr_prefetch(a.codes + pf.row * (16 * a.pw), n * (16 * a.pw));
+                    tr_prefetch(a.norms + pf.row, n * 2);
+                }
+            }
+            if (++npf < count) pf.next(a);
+        };
+        while (npf < count && npf < kTrAhead) fetch();
+        for (int c = 0; c < count && ok; ++c) {
+            if (npf < count) fetch();
+            const int b = c & 1, pb = np == 2 ? b : 0;
             if (fresh && seg++ > 0 && !mbar_wait(o_empty, (uint32_t)((seg - 2) & 1))) { ok = false; break; }
             if (!mbar_wait(&v_full[b], (uint32_t)((c >> 1) & 1))) { ok = false; break; }
             if (!mbar_wait(&p_full[b], (uint32_t)((c >> 1) & 1))) { ok = false; break; }
             tc_fence_after();
-            if (lane == 0) {
+            if (tr_elect()) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_f16(tO, tr_sdesc(sV0 + (uint32_t)b * kTrVBytes + kk * 2048u, kTrVBytes / 2, 1024u),
+                    mma_f16(tO, tr_sdesc(sV0 + (uint32_t)(nv == 2 ? b : 0) * kTrVBytes + kk * 2048u, kTrVBytes / 2, 1024u),
                             tr_sdesc(sP0 + (uint32_t)pb * (uint32_t)tr_pbytes(NB) + kk * 2048u, kTrTok * 128u, 1024u), idesc,
                             (fresh && kk == 0) ? 0u : 1u);
-                mma_commit(&pv_done[b]);
+                // sums of the weights over the tokens, [row][16 equal columns]: P^T times ones.  (Up to 64 rows the
+                // second half of the operand's 128 rows is whatever lies 8 tokens further: rows that nobody reads.)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_f16(tL, tr_sdesc(sP0 + (uint32_t)pb * (uint32_t)tr_pbytes(NB) + kk * 2048u, NB == 128 ? kTrTok * 128u : 1024u, 1024u),
+                            sdesc_k_sw128(ones0), idesc_f16(false, 128, 16) | (1u << 15), (fresh && kk == 0) ? 0u : 1u);
+                mma_commit(&pv_done[c & 3]);
             }
             __syncwarp();
-            fresh = c + 1 < count && it.next(a.off, a.rbs);
+            fresh = c + 1 < count && it.next(a);
         }
-    } else if (count > 0 && warp < 8) {
+    } else if (count > 0 && warp < SW) {
         // ------------------------------------------------------------ softmax
-        const int w = warp >> 2, cb = w * CW, wt = tid & 127, bar = 1 + w;
+        const int wg = warp >> 2, cb = wg * 32, wt = tid & 127, bar = 1 + wg;     // rows cb .. cb + 31
         const int r = (int)quarter * 32 + lane;                 // token of the tile
-        const uint32_t lanes = quarter << 21;
-        const float kq = 1.2533141373155002512f / (float)a.m;
-        const uint16_t *gsrc = two ? a.norms : a.sk_norms;
-        const float gk = two ? 1.0f / (float)kTrD : kq;
-        auto load_g = [&](const TreeIter &p) {
-            const int64_t t = p.tile * kTrTok + r;
-            return t < tr_len(a, p.g) ? h16_to_f32(__ldg(gsrc + p.g * a.T + t)) : -1.0f;   // norms are >= 0
-        };
-        float gn = load_g(it);
-        float ref = -INFINITY;                                  // of column wt < CW
-        float l[NCH == 2 ? 2 : CW];
-        const float4 *F = reinterpret_cast<const float4 *>(sF) + cb / 2;
+        const uint32_t lanes = quarter << 21, sP0 = smem_u32(sP), sF0 = smem_u32(sF) + (uint32_t)cb * 8u;
+        const uint16_t *gsrc = TWO ? a.norms : a.sk_norms;
+        const float gk = TWO ? 1.0f / (float)kTrD : 1.2533141373155002512f / (float)a.m * kTrBitScale;
+        uint16_t gn = r < it.left ? __ldg(gsrc + it.row + r) : (uint16_t)0;
+        float ref = -INFINITY, cq = 0.0f;                       // reference of row cb + wt (wt < 32); the chunk's factor
         bool fresh = true;
-        for (int64_t c = 0; c < count; ++c) {                   // every item and barrier also after a wait has expired
-            const int sb = (int)(c & 1);
-            const int64_t pg = it.g * a.rbs + it.rb;
+        uint32_t use = 0;                                       // votes so far
+        for (int c = 0; c < count; ++c) {                       // every item and barrier also after a wait has expired
             const bool start = fresh;
             if (start) {
-                if (wt < CW) {
-                    const float cq = __ldg(a.wsC + pg * NB + cb + wt);
-                    float *f = sF + ((cb + wt) >> 1) * 4 + (wt & 1);
-                    f[0] = cq;
+                if (wt < 32) {
+                    const int row = cb + wt;
+                    float sum = 0.0f;
+                    if (!TWO) {
+                        const float *wc = a.wsC + ((int64_t)a.G * a.rbs + it.g * a.rbs + it.rb) * NB + row;
+                        for (int i = 0; i < 2 * nsl; ++i) sum += wc[(int64_t)i * a.G * a.rbs * NB];
+                    }
+                    float *f = reinterpret_cast<float *>(sF + (row >> 1)) + (row & 1);
+                    f[0] = sum * (-1.0f / kTrBitScale);
                     f[2] = 0.0f;
                 }
                 ref = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < (NCH == 2 ? 2 : CW); ++j) l[j] = 0.0f;
+                cq = a.wsC[(it.g * a.rbs + it.rb) * NB + cb];
                 tr_bar(bar);
             }
-            const bool valid = gn >= 0.0f;
-            const float g = valid ? __fmul_rn(gn, gk) : 0.0f;
-            TreeIter nx = it;
+            const bool valid = r < it.left;
+            const float gg = __fmul_rn(__fmul_rn(h16_to_f32(gn), gk), cq);
+            const uint32_t vm = valid ? 0xffffffffu : 0u;
+            const int64_t pg = it.g * a.rbs + it.rb;
             fresh = false;
             if (c + 1 < count) {
-                fresh = nx.next(a.off, a.rbs);
-                gn = load_g(nx);
+                fresh = it.next(a);
+                gn = r < it.left ? __ldg(gsrc + it.row + r) : (uint16_t)0;
             }
-            if (ok && !mbar_wait(&s_full[sb], (uint32_t)((c >> 1) & 1))) ok = false;
+            if (ok && !mbar_wait(&s_full[c & 1], (uint32_t)((c >> 1) & 1))) ok = false;
             tc_fence_after();
-            uint32_t sr[CW];
-            const uint32_t src = tS + (uint32_t)(sb * NB + cb) + lanes;
-            auto load_s = [&]() {
-                if constexpr (CW == 16) {
-                    tmem_ld16(src, sr);
-                } else {
+            uint32_t sr[32], w[16];                             // scores, then exponents; fp16 weights of row pairs
+            tmem_ld32(tS + (uint32_t)(c % NS * NB + cb) + lanes, sr);
+            tmem_ld_wait();
+            tc_fence_before();                                  // the scores are read
+            __syncwarp();
+            if (lane == 0) tr_arrive(&s_empty[c & 1]);
+            // exponents (s - Q) gg + (8 - ref) (at the start of a segment: before any reference) and their maximum
+            float mx = -INFINITY;
 #pragma unroll
-                    for (int ch = 0; ch < NCH; ++ch) tmem_ld32(src + 32u * ch, sr + 32 * ch);
+            for (int j = 0; j < 32; j += 2) {
+                const float4 f = tr_lds_f4(sF0 + (uint32_t)j * 8u);
+                const float2 off = TWO ? make_float2(f.z, f.w)
+                                       : __ffma2_rn(make_float2(f.x, f.y), make_float2(gg, gg), make_float2(f.z, f.w));
+                const float2 v = __ffma2_rn(make_float2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])),
+                                            make_float2(gg, gg), off);
+                sr[j] = __float_as_uint(v.x);
+                sr[j + 1] = __float_as_uint(v.y);
+                mx = fmaxf(fmaxf(mx, v.x), v.y);
+            }
+            auto weights = [&]() {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const __half2 h = __floats2half2_rn(tr_ex2(__uint_as_float(sr[2 * j])), tr_ex2(__uint_as_float(sr[2 * j + 1])));
+                    w[j] = *reinterpret_cast<const uint32_t *>(&h) & vm;
                 }
-                tmem_ld_wait();
             };
-            // exponents a = s g cq + (8 - ref), in place of s; returns their maximum
-            auto exponents = [&]() {
-                float mx = -INFINITY;
+            bool slow = start;
+            if (!start) {
+                // The group's vote, taken while the weights are computed for the usual answer.  (A flag belongs to
+                // one use: written with its number, in two places in turn.)
+                ++use;
+                if (valid && mx > kTrMost) flag[2 * wg + (use & 1)] = use;
+                __syncwarp();
+                if (lane == 0) tr_arrive(&vote[wg]);
+                weights();
+                if (ok && !mbar_wait(&vote[wg], (use - 1) & 1)) ok = false;
+                slow = flag[2 * wg + (use & 1)] == use;
+            }
+            if (slow) {
+                // new references: the maxima over the tile's tokens
+                uint32_t t[32];
 #pragma unroll
-                for (int j = 0; j < CW; j += 2) {
-                    const float4 f = F[j >> 1];
-                    const float2 x = __fmul2_rn(make_float2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), make_float2(g, g));
-                    const float2 v = __ffma2_rn(x, make_float2(f.x, f.y), make_float2(f.z, f.w));
-                    sr[j] = __float_as_uint(v.x);
-                    sr[j + 1] = __float_as_uint(v.y);
-                    mx = fmaxf(fmaxf(mx, v.x), v.y);
-                }
-                return mx;
-            };
-            load_s();
-            const float mx = exponents();
-            if (tr_bar_or(bar, start || (valid && mx > kTrMost))) {
-                // new references: the maxima over the tile's tokens of s g cq
-                float *X = sX + quarter * NB + cb;
-#pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    uint32_t t32[CH];
-                    if constexpr (CH == 16) tmem_ld16(src, t32);
-                    else tmem_ld32(src + 32u * ch, t32);
-                    tmem_ld_wait();
-                    float v[CH];
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) {
-                        const float cq = sF[((cb + ch * CH + j) >> 1) * 4 + (j & 1)];
-                        v[j] = valid ? __fmul_rn(__fmul_rn(__uint_as_float(t32[j]), g), cq) : -INFINITY;
-                    }
-                    const float x = tr_reduce_columns<CH>(v, lane, [](float p, float q) { return fmaxf(p, q); });
-                    if (lane < CH) X[ch * CH + lane] = x;
-                }
+                for (int j = 0; j < 32; ++j) t[j] = valid ? sr[j] : 0xff800000u;
+                sX[quarter * NB + cb + lane] = tr_reduce_columns(t, lane, [](float p, float q) { return fmaxf(p, q); });
                 tr_bar(bar);
-                if (wt < CW) {
+                if (wt < 32) {
                     const float *x = sX + cb + wt;
-                    const float mn = fmaxf(ref, fmaxf(fmaxf(x[0], x[NB]), fmaxf(x[2 * NB], x[3 * NB])));
+                    float *off = reinterpret_cast<float *>(sF + ((cb + wt) >> 1)) + 2 + (wt & 1);
+                    const float old = *off;                     // 8 - ref, 0 at the start
+                    const float mn = fmaxf(ref, fmaxf(fmaxf(x[0], x[NB]), fmaxf(x[2 * NB], x[3 * NB])) - old);
                     sAl[cb + wt] = ref == -INFINITY ? 0.0f : tr_ex2(ref - mn);
-                    sF[((cb + wt) >> 1) * 4 + 2 + (wt & 1)] = kTrShift - mn;
+                    sX[4 * NB + cb + wt] = (kTrShift - mn) - old;               // what the exponents move by
+                    *off = kTrShift - mn;
                     ref = mn;
                 }
                 tr_bar(bar);
-                if constexpr (NCH == 2) {
-                    l[0] *= sAl[cb + lane];
-                    l[1] *= sAl[cb + 32 + lane];
-                } else {
 #pragma unroll
-                    for (int j = 0; j < CW; ++j) l[j] *= sAl[cb + j];
-                }
-                if (!start) {                                   // O of the segment's earlier tiles
-                    if (ok && !mbar_wait(&pv_done[(c - 1) & 1], (uint32_t)(((c - 1) >> 1) & 1))) ok = false;
+                for (int j = 0; j < 32; ++j) sr[j] = __float_as_uint(__uint_as_float(sr[j]) + sX[4 * NB + cb + j]);
+                weights();
+                if (!start) {                                   // O and the sums of the segment's earlier tiles
+                    if (ok && !pv_wait(c - 1)) ok = false;
                     tc_fence_after();
-#pragma unroll
-                    for (int ch = 0; ch < CW / 16; ++ch) {
-                        uint32_t o[16];
-                        const uint32_t at = tO + (uint32_t)(cb + 16 * ch) + lanes;
-                        tmem_ld16(at, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__fmul_rn(__uint_as_float(o[j]), sAl[cb + 16 * ch + j]));
-                        tmem_st16(at, o);
-                    }
-                    tmem_st_wait();
-                }
-                load_s();
-                exponents();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tr_arrive(&s_empty[sb]);
-            // weights: row r of the [token][row] operand
-            if (np == 2) {
-                if (c >= 2 && ok && !mbar_wait(&pv_done[sb], (uint32_t)(((c >> 1) - 1) & 1))) ok = false;
-            } else {
-                if (c >= 1 && ok && !mbar_wait(&pv_done[(c - 1) & 1], (uint32_t)(((c - 1) >> 1) & 1))) ok = false;
-            }
-            uint8_t *Pr = sP + (size_t)(np == 2 ? sb : 0) * tr_pbytes(NB) + (size_t)(cb >> 6) * (kTrTok * 128) +
-                          (size_t)(r >> 3) * 1024 + (size_t)(r & 7) * 128;
-            const int ch0 = (cb & 63) >> 3;                     // 16-byte chunk of this half's first row
-#pragma unroll
-            for (int ch = 0; ch < CW / 8; ++ch) {
-                uint32_t w4[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 8 * ch + 2 * e;
-                    const float p0 = valid ? tr_ex2(__uint_as_float(sr[j])) : 0.0f;
-                    const float p1 = valid ? tr_ex2(__uint_as_float(sr[j + 1])) : 0.0f;
-                    const __half2 h = __floats2half2_rn(p0, p1);
-                    w4[e] = *reinterpret_cast<const uint32_t *>(&h);
-                    if constexpr (NCH == 2) {
-                        sr[j] = __float_as_uint(p0);
-                        sr[j + 1] = __float_as_uint(p1);
-                    } else {
-                        l[j] += p0;
-                        l[j + 1] += p1;
-                    }
-                }
-                *reinterpret_cast<uint4 *>(Pr + (((ch0 + ch) ^ (r & 7)) << 4)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tr_arrive(&p_full[sb]);
-            if constexpr (NCH == 2) {                           // sums over the warp's tokens, column `lane` of each chunk
-                auto add = [](float p, float q) { return p + q; };
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sr[32 * ch + j]);
-                    l[ch] += tr_reduce_columns<32>(v, lane, add);
-                }
-            }
-            if (fresh || c + 1 == count) {                      // end of the segment
-                if (ok && !mbar_wait(&pv_done[sb], (uint32_t)((c >> 1) & 1))) ok = false;
-                tc_fence_after();
-                float *part = a.part + (size_t)(blockIdx.x + pg) * tr_part_floats(NB);
-#pragma unroll
-                for (int ch = 0; ch < CW / 16; ++ch) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + (uint32_t)(cb + 16 * ch) + lanes, o);
+                    const uint32_t at = tO + (uint32_t)cb + lanes;
+                    tmem_ld32(at, t);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(size_t)(cb + 16 * ch + j) * kTrD + r] = __uint_as_float(o[j]);
+                    for (int j = 0; j < 32; ++j) t[j] = __float_as_uint(__fmul_rn(__uint_as_float(t[j]), sAl[cb + j]));
+                    tmem_st32(at, t);
+                    if (quarter == (uint32_t)(wg & 3)) {        // rows are the sums' lanes
+                        const uint32_t x = tmem_ld1(tL + lanes);
+                        tmem_ld_wait();
+                        tmem_st1(tL + lanes, __float_as_uint(__fmul_rn(__uint_as_float(x), sAl[cb + lane])));
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
                 }
+            }
+            if (c >= np && ok && !pv_wait(c - np)) ok = false;  // the tile whose weights lie in the buffer
+            // row r of the [token][row] operand
+            const uint32_t Pr = sP0 + (np == 2 ? (uint32_t)(c & 1) * (uint32_t)tr_pbytes(NB) : 0u) +
+                                (uint32_t)(cb >> 6) * (kTrTok * 128u) + (uint32_t)r * 128u;
+            const int ch0 = (cb & 63) >> 3;                     // 16-byte chunk of this group's first row
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tr_sts128(Pr + (uint32_t)(((ch0 + k) ^ (r & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tr_arrive(&p_full[c & 1]);
+            if (fresh || c + 1 == count) {                      // end of the segment
+                if (ok && !pv_wait(c)) ok = false;
+                tc_fence_after();
+                float *part = a.part + (size_t)(blockIdx.x + pg) * tr_part_floats(NB);
+                tmem_ld32(tO + (uint32_t)cb + lanes, sr);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) part[(size_t)(cb + j) * kTrD + r] = __uint_as_float(sr[j]);
+                if (quarter == (uint32_t)(wg & 3)) {
+                    const uint32_t x = tmem_ld1(tL + lanes);
+                    tmem_ld_wait();
+                    part[(size_t)NB * kTrD + NB + cb + lane] = __uint_as_float(x);
+                }
+                if (wt < 32) part[(size_t)NB * kTrD + cb + wt] = ref - kTrShift;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tr_arrive(o_empty);
-                float *X = sX + quarter * NB + cb;
-                if constexpr (NCH == 2) {
-                    X[lane] = l[0];
-                    X[32 + lane] = l[1];
-                } else {
-                    const float x = tr_reduce_columns<CW>(l, lane, [](float p, float q) { return p + q; });
-                    if (lane < CW) X[lane] = x;
-                }
-                tr_bar(bar);
-                if (wt < CW) {
-                    const float *x = sX + cb + wt;
-                    part[(size_t)NB * kTrD + cb + wt] = ref - kTrShift;
-                    part[(size_t)NB * kTrD + NB + cb + wt] = (x[0] + x[NB]) + (x[2 * NB] + x[3 * NB]);
-                }
-                tr_bar(bar);
+                tr_bar(bar);                                    // the next segment rewrites the rows' constants
             }
-            it = nx;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 16) tmem_dealloc(tmem, 512);
+    if (warp == SW + PW) tmem_dealloc(tmem, tr_tmem(NB));
 }
 
 // ------------------------------------------------------------------ prologue
@@ -713,7 +814,7 @@ __device__ __forceinline__ const uint16_t *tr_row(const uint16_t *p, const rq_st
 }
 
 // Grid (32-row tiles of every row block, 64-column slices); 4 warps, each 16 rows x 32 columns of
-//   [q H D ; q S^T] / |q|
+//   [q H D ; q S^T] / max |q| of the 32 rows
 // as bf16 products with fp32 sums: the entries of H D are +-1, an fp16 projection is the sum of two bf16 numbers, so
 // every product is exact.  A thread's 128-value rows are loaded as 64 contiguous bytes a lane of the quad; the sum
 // over k runs in that order for both operands.  CTA (0, 0) also writes the prefix sums of the groups' tiles.
@@ -721,6 +822,7 @@ __global__ void __launch_bounds__(128)
 tree_prologue_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ QuantTables TK)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = lane & 3, rr = lane >> 2;
+    tr_launch_next();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         __shared__ int64_t sums[128];
         int64_t run = 0;
@@ -776,12 +878,32 @@ tree_prologue_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__
         ss[h] += __shfl_xor_sync(0xffffffffu, ss[h], 1);
         ss[h] += __shfl_xor_sync(0xffffffffu, ss[h], 2);
     }
+    // one factor for the chunk's 32 rows, the largest finite |q| (a row whose own is not finite comes out NaN by itself)
+    __shared__ float norm[32];
     const float n0 = sqrtf(ss[0]), n1 = sqrtf(ss[1]);
-    const float i0 = n0 > 0.0f ? 1.0f / n0 : 0.0f, i1 = n1 > 0.0f ? 1.0f / n1 : 0.0f;
-    if (s == 0 && p == 0 && (warp >> 1) == 0) {
-        a.wsC[pg * a.nb + row0 + rr] = n0 * a.qscale;
-        a.wsC[pg * a.nb + row0 + rr + 8] = n1 * a.qscale;
+    if (p == 0) {
+        norm[(warp & 1) * 16 + rr] = n0 < INFINITY ? n0 : 0.0f;
+        norm[(warp & 1) * 16 + rr + 8] = n1 < INFINITY ? n1 : 0.0f;
     }
+    __syncthreads();
+    float nmax = norm[lane];
+    for (int o = 16; o > 0; o >>= 1) nmax = fmaxf(nmax, __shfl_xor_sync(0xffffffffu, nmax, o));
+    const float inv = nmax > 0.0f ? 1.0f / nmax : 0.0f;
+    if (s == 0 && tid == 0) a.wsC[pg * a.nb + row0] = nmax * a.qscale;
+    uint32_t Bs[4][16];                                         // four operand rows, loaded at once
+    if (s >= dsl) {
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8) {
+            const int c = (warp >> 1) * 32 + n8 * 8 + rr;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.proj + (int64_t)((s - dsl) * 64 + c) * kTrD + 32 * p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(src + i);
+                Bs[n8][4 * i] = v.x; Bs[n8][4 * i + 1] = v.y; Bs[n8][4 * i + 2] = v.z; Bs[n8][4 * i + 3] = v.w;
+            }
+        }
+    }
+    float part[2] = {0.0f, 0.0f};
     uint8_t *img = a.wsQ + pg * (int64_t)a.nb * a.kb * 2 + (int64_t)s * a.nb * 128;
 #pragma unroll
     for (int n8 = 0; n8 < 4; ++n8) {
@@ -803,13 +925,7 @@ tree_prologue_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__
                 tr_mma_bf16(d, af, b[0], b[1]);
             }
         } else {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.proj + (int64_t)((s - dsl) * 64 + c) * kTrD + 32 * p);
-            uint32_t B[16];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldg(src + i);
-                B[4 * i] = v.x; B[4 * i + 1] = v.y; B[4 * i + 2] = v.z; B[4 * i + 3] = v.w;
-            }
+            const uint32_t *B = Bs[n8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const uint32_t af[4] = {A[0][2 * k], A[1][2 * k], A[0][2 * k + 1], A[1][2 * k + 1]};
@@ -834,150 +950,204 @@ tree_prologue_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__
         for (int e = 0; e < 4; ++e) {
             const int r = row0 + rr + (e >> 1) * 8;
             int col = (warp >> 1) * 32 + n8 * 8 + 2 * p + (e & 1);
+            float x = d[e] * inv;
+            const float f = tr_bit_factor(col);
+            if (!a.pw) x *= f;                                   // by a power of two
+            const __half h = __float2half_rn(x);
+            if (!a.pw) part[e >> 1] += __half2float(h) / f;
             if (s >= dsl) col = tr_sign_column(col);
-            *reinterpret_cast<__half *>(img + (r >> 3) * 1024 + (r & 7) * 128 + (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2) =
-                __float2half_rn(d[e] * ((e >> 1) ? i1 : i0));
+            *reinterpret_cast<__half *>(img + (r >> 3) * 1024 + (r & 7) * 128 + (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2) = h;
+        }
+    }
+    if (!a.pw) {                                                 // sums of the rounded coordinates of each row, by 32
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            part[h] += __shfl_xor_sync(0xffffffffu, part[h], 1);
+            part[h] += __shfl_xor_sync(0xffffffffu, part[h], 2);
+            if (p == 0)
+                a.wsC[((int64_t)(1 + 2 * s + (warp >> 1)) * a.G * a.rbs + pg) * a.nb + row0 + rr + 8 * h] = part[h];
         }
     }
 }
 
 // ------------------------------------------------------------------ combine
 
-constexpr int kTrCombineRows = 4;
+constexpr int kTrCombineRows = 16;
+constexpr int kTrCombineThreads = 256;
+constexpr int kTrCombineSlots = 16;               // segments joined at a time
 
-// A CTA of 128 threads (thread = coordinate) joins four rows of a group: their drafted part in fp32 from the 16-bit
-// keys and values, then their segments of the cached part (m, l, O), rotated back by H and D.
-__global__ void __launch_bounds__(128)
+// A CTA joins 16 rows of a group.  Drafted part: the scores of 16 rows and 8 nodes a warp by bf16 products, a softmax
+// by warps, then thread = (coordinate, 8 rows) over the values, all before the cached part has to be there.  Cached
+// part: the weights of up to 16 segments at once, then the segments' rows, loads in flight together; rotated back by H
+// and D, divided, rounded.
+__global__ void __launch_bounds__(kTrCombineThreads)
 tree_combine_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ QuantTables TV, int grid_main)
 {
-    extern __shared__ float sS[];                               // [4][n_nodes] scores, then weights
-    __shared__ float sm[4], sl[4], buf[4][kTrD];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    extern __shared__ __align__(16) float sS[];                 // [nodes][16] scores, then weights
+    __shared__ float sM[16], sL[16], sScale[16];
+    __shared__ __align__(16) float sW[kTrCombineSlots][16];
+    __shared__ float buf[16][kTrD];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, p = lane & 3, rr = lane >> 2;
     const int64_t g = blockIdx.y;
     const int r0 = blockIdx.x * kTrCombineRows, n = a.nodes;
     const int64_t b = g / a.kv_heads;
     const int kv = (int)(g - b * a.kv_heads);
-    const uint64_t *mask = a.mask ? a.mask + b * a.mask_batch : nullptr;
-    const int words = (n + 63) / 64;
-    auto sees = [&](int r, int j) -> bool {
-        if (r >= a.rows) return false;
-        const int node = r / a.rep;
-        return mask ? (__ldg(mask + (int64_t)node * words + (j >> 6)) >> (j & 63)) & 1u : j <= node;
-    };
-    // scores (in units of log2)
     {
-        float q[4][4];
+        uint32_t A[2][16];
+        const uint64_t *mrow[2];
+        int node[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint2 v = make_uint2(0u, 0u);
-            if (r0 + i < a.rows) v = __ldg(reinterpret_cast<const uint2 *>(tr_row(a.q, a.qs, a, g, r0 + i)) + lane);
-            q[i][0] = bf16_lo(v.x); q[i][1] = bf16_hi(v.x); q[i][2] = bf16_lo(v.y); q[i][3] = bf16_hi(v.y);
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + rr + 8 * h;
+            const bool in = r < a.rows;
+            node[h] = in ? r / a.rep : -1;
+            mrow[h] = a.mask && in ? a.mask + b * a.mask_batch + (int64_t)node[h] * ((n + 63) / 64) : nullptr;
+            const uint4 *src = in ? reinterpret_cast<const uint4 *>(tr_row(a.q, a.qs, a, g, r) + 32 * p) : nullptr;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                A[h][4 * i] = v.x; A[h][4 * i + 1] = v.y; A[h][4 * i + 2] = v.z; A[h][4 * i + 3] = v.w;
+            }
         }
-        for (int j = warp; j < n; j += 4) {
-            bool any = false;
-            bool vis[4];
+        for (int j0 = 8 * warp; j0 < n; j0 += 64) {
+            uint32_t B[16];
+            const bool in = j0 + rr < n;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.k_new + b * a.ks.batch + (int64_t)(in ? j0 + rr : 0) * a.ks.token +
+                                                               (int64_t)kv * a.ks.head + 32 * p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) { vis[i] = sees(r0 + i, j); any |= vis[i]; }
-            float dot[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (any) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(a.k_new + b * a.ks.batch + (int64_t)j * a.ks.token + (int64_t)kv * a.ks.head) + lane);
-                const float k0 = bf16_lo(v.x), k1 = bf16_hi(v.x), k2 = bf16_lo(v.y), k3 = bf16_hi(v.y);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(src + i);
+                B[4 * i] = v.x; B[4 * i + 1] = v.y; B[4 * i + 2] = v.z; B[4 * i + 3] = v.w;
+            }
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x = __fmaf_rn(q[i][0], k0, __fmaf_rn(q[i][1], k1, __fmaf_rn(q[i][2], k2, q[i][3] * k3)));
-                    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                    dot[i] = vis[i] ? x * a.qscale : -INFINITY;
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t af[4] = {A[0][2 * k], A[1][2 * k], A[0][2 * k + 1], A[1][2 * k + 1]};
+                tr_mma_bf16(d, af, B[2 * k], B[2 * k + 1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t bits = mrow[h] ? (uint32_t)(__ldg(mrow[h] + (j0 >> 6)) >> (j0 & 63)) : 0u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = j0 + 2 * p + e;
+                    const bool sees = a.mask ? (bits >> (2 * p + e)) & 1u : j <= node[h];
+                    if (j < n) sS[j * 16 + rr + 8 * h] = sees ? d[2 * h + e] * a.qscale : -INFINITY;
                 }
             }
-            if (lane < 4) sS[lane * n + j] = lane == 0 ? dot[0] : lane == 1 ? dot[1] : lane == 2 ? dot[2] : dot[3];
         }
     }
     __syncthreads();
-    {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {                               // softmax of rows 2 warp, 2 warp + 1
+        const int row = 2 * warp + i;
         float m = -INFINITY, l = 0.0f;
-        for (int j = lane; j < n; j += 32) m = fmaxf(m, sS[warp * n + j]);
+        for (int j = lane; j < n; j += 32) m = fmaxf(m, sS[j * 16 + row]);
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         for (int j = lane; j < n; j += 32) {
-            const float s = sS[warp * n + j];
-            const float p = s == -INFINITY ? 0.0f : tr_ex2(s - m);       // (a NaN score stays one)
-            sS[warp * n + j] = p;
-            l += p;
+            const float s = sS[j * 16 + row];
+            const float w = s == -INFINITY ? 0.0f : tr_ex2(s - m);       // (a NaN score stays one)
+            sS[j * 16 + row] = w;
+            l += w;
         }
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+        if (lane == 0) { sM[row] = m; sL[row] = l; }
     }
     __syncthreads();
-    float ot[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const uint16_t *vcol = a.v_new + b * a.vs.batch + (int64_t)kv * a.vs.head + tid;
+    const int d = tid & (kTrD - 1), h0 = (tid >> 7) * 8;        // coordinate, first of this thread's 8 rows
+    float ot[8], acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ot[i] = acc[i] = 0.0f;
+    const uint16_t *vcol = a.v_new + b * a.vs.batch + (int64_t)kv * a.vs.head + d;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
-        const float p0 = sS[j], p1 = sS[n + j], p2 = sS[2 * n + j], p3 = sS[3 * n + j];
-        if (p0 == 0.0f && p1 == 0.0f && p2 == 0.0f && p3 == 0.0f) continue;
         const float v = __uint_as_float((uint32_t)__ldg(vcol + (int64_t)j * a.vs.token) << 16);
-        // a hidden value may be anything: it is not touched
-        if (p0 != 0.0f) ot[0] = __fmaf_rn(p0, v, ot[0]);
-        if (p1 != 0.0f) ot[1] = __fmaf_rn(p1, v, ot[1]);
-        if (p2 != 0.0f) ot[2] = __fmaf_rn(p2, v, ot[2]);
-        if (p3 != 0.0f) ot[3] = __fmaf_rn(p3, v, ot[3]);
+        const float4 w0 = *reinterpret_cast<const float4 *>(sS + j * 16 + h0), w1 = *reinterpret_cast<const float4 *>(sS + j * 16 + h0 + 4);
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (w[i] != 0.0f) ot[i] = __fmaf_rn(w[i], v, ot[i]);         // a hidden value may be anything: it is not used
     }
-    // segments of the row block: CTAs whose ranges [total c / grid, total (c + 1) / grid) meet its items
     const int rb = r0 / a.nb;
     const int64_t pg = g * a.rbs + rb;
-    float M[4], L[4], acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { M[i] = sm[i]; L[i] = sl[i]; acc[i] = 0.0f; }
-    if (grid_main > 0) {
-        const int64_t total = a.off[a.G] * a.rbs, tiles = a.off[g + 1] - a.off[g];
-        const int64_t lo = a.off[g] * a.rbs + rb * tiles, hi = lo + tiles;
-        if (tiles > 0) {
-            int c = (int)((lo * grid_main) / total);
-            while (c > 0 && total * c / grid_main > lo) --c;
-            while (total * (c + 1) / grid_main <= lo) ++c;
-            for (; c < grid_main && total * c / grid_main < hi; ++c) {
-                if (total * (c + 1) / grid_main <= total * c / grid_main) continue;     // an empty range
-                const float *P = a.part + (size_t)(c + pg) * tr_part_floats(a.nb);
-                const int in = r0 - rb * a.nb;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float m = P[(size_t)a.nb * kTrD + in + i], l = P[(size_t)a.nb * kTrD + a.nb + in + i];
-                    const float mn = fmaxf(M[i], m);
-                    const float wo = M[i] == -INFINITY ? 0.0f : tr_ex2(M[i] - mn), wn = tr_ex2(m - mn);
-                    L[i] = __fmaf_rn(L[i], wo, l * wn);
-                    ot[i] *= wo;
-                    acc[i] = __fmaf_rn(acc[i], wo, P[(size_t)(in + i) * kTrD + tid] * wn);
-                    M[i] = mn;
+    tr_wait_previous();
+    int64_t tiles = 0;
+    if (grid_main > 0) tiles = a.off[g + 1] - a.off[g];
+    if (tiles > 0) {
+        // the CTA of an item: the largest c with total c / ctas <= item
+        const int64_t total = a.off[a.G] * a.rbs, ctas = total < grid_main ? total : grid_main;
+        const int64_t lo = a.off[g] * a.rbs + rb * tiles, hi = lo + tiles - 1;
+        const int c_lo = (int)(((lo + 1) * ctas - 1) / total), c_hi = (int)(((hi + 1) * ctas - 1) / total);
+        const int in = r0 - rb * a.nb;
+        for (int c = c_lo; c <= c_hi; c += kTrCombineSlots) {
+            const int ns = c_hi - c + 1 < kTrCombineSlots ? c_hi - c + 1 : kTrCombineSlots;
+            const float *P = a.part + (size_t)(c + pg) * tr_part_floats(a.nb);
+            {
+                const int row = tid >> 4, slot = tid & 15;
+                const float *q = P + (size_t)slot * tr_part_floats(a.nb) + (size_t)a.nb * kTrD + in + row;
+                const float m = slot < ns ? q[0] : -INFINITY, l = slot < ns ? q[a.nb] : 0.0f, old = sM[row];
+                float mx = m;
+                for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                mx = fmaxf(mx, old);
+                const float w = m == -INFINITY ? 0.0f : tr_ex2(m - mx);
+                float sum = w * l;
+                for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                sW[slot][row] = w;
+                if (slot == 0) {
+                    const float sc = old == -INFINITY ? 0.0f : tr_ex2(old - mx);
+                    sScale[row] = sc;
+                    sL[row] = __fmaf_rn(sL[row], sc, sum);
+                    sM[row] = mx;
                 }
             }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                ot[i] *= sScale[h0 + i];
+                acc[i] *= sScale[h0 + i];
+            }
+            const float *O = P + (size_t)(in + h0) * kTrD + d;
+#pragma unroll 2
+            for (int s = 0; s < ns; ++s, O += tr_part_floats(a.nb)) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = O[i * kTrD];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(x[i], sW[s][h0 + i], acc[i]);
+            }
+            __syncthreads();
+        }
+        // H over the 128 coordinates: stages inside the warp, then across the warps
+#pragma unroll
+        for (int h = 1; h < 32; h <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float o = __shfl_xor_sync(0xffffffffu, acc[i], h);
+                acc[i] = (lane & h) ? o - acc[i] : acc[i] + o;
+            }
+        }
+#pragma unroll
+        for (int h = 32; h < kTrD; h <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) buf[h0 + i][d] = acc[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float o = buf[h0 + i][d ^ h];
+                acc[i] = (d & h) ? o - acc[i] : acc[i] + o;
+            }
+            __syncthreads();
         }
     }
-    // H over the 128 coordinates: stages inside the warp, then across the warps
+    const bool neg = (TV.sign_words[d >> 5] >> (d & 31)) & 1u;
 #pragma unroll
-    for (int h = 1; h < 32; h <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float o = __shfl_xor_sync(0xffffffffu, acc[i], h);
-            acc[i] = (lane & h) ? o - acc[i] : acc[i] + o;
-        }
-    }
-#pragma unroll
-    for (int h = 32; h < kTrD; h <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) buf[i][tid] = acc[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float o = buf[i][tid ^ h];
-            acc[i] = (tid & h) ? o - acc[i] : acc[i] + o;
-        }
-        __syncthreads();
-    }
-    const bool neg = (TV.sign_words[tid >> 5] >> (tid & 31)) & 1u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (r0 + i >= a.rows) break;
-        const float x = (neg ? -acc[i] : acc[i]) + ot[i];
-        const float y = L[i] == 0.0f ? 0.0f : __fdiv_rn(x, L[i]);
-        uint16_t *dst = const_cast<uint16_t *>(tr_row(a.out, a.os, a, g, r0 + i));
-        dst[tid] = (uint16_t)(pack2<true>(y, 0.0f) & 0xffffu);
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + h0 + i;
+        if (r >= a.rows) break;
+        const float x = (neg ? -acc[i] : acc[i]) + ot[i], l = sL[h0 + i];
+        const float y = l == 0.0f ? 0.0f : __fdiv_rn(x, l);
+        uint16_t *dst = const_cast<uint16_t *>(tr_row(a.out, a.os, a, g, r));
+        dst[d] = (uint16_t)(pack2<true>(y, 0.0f) & 0xffffu);
     }
 }
 

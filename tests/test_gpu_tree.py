@@ -166,6 +166,29 @@ def test_against_float64(B, KV, rep, n, T, m, kbits, vbits, ragged):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("rows,m,kbits,vbits", [(30, 256, 0, 4), (39, 128, 2, 3), (60, 192, 0, 4), (64, 512, 4, 8), (100, 256, 0, 4),
+                                                (128, 256, 3, 2), (32, 512, 1, 4), (33, 64, 2, 4)])
+def test_many_tiles_per_cta(rows, m, kbits, vbits):
+    """Enough cached tokens that every CTA runs tens of tiles and its buffers wrap many times, in several row blocks
+    and groups; sampled groups against float64."""
+    B, KV, T = 24, 2, 20011
+    c = compress(B * KV, T, D, m, kbits, vbits, 400 + rows, kbits > 0,
+                 vlayout=L.RQ_CODES_INT8 if vbits == 8 else L.RQ_CODES_PACKED)
+    q, kn, vn = drafted(B, rows, KV, 1, rows)
+    lens = torch.tensor([T - 97 * i for i in range(B * KV)], dtype=torch.int32, device=DEV)
+    scale = 1 / math.sqrt(D)
+    got = run(c, q, kn, vn, None, m, T, lens, kbits, vbits, scale)
+    torch.cuda.synchronize()
+    assert L.rq_device_error(True) == 0
+    for b in (0, 11, B - 1):
+        part = {k: (v[b * KV * (v.shape[0] // (B * KV)):(b + 1) * KV * (v.shape[0] // (B * KV))]
+                    if isinstance(v, torch.Tensor) and k not in ("k", "v", "S") else v) for k, v in c.items()}
+        kt, vt = vectors(part, KV, T, m, kbits, vbits)
+        check(got[b:b + 1], kt, vt, q[b:b + 1], kn[b:b + 1], vn[b:b + 1], None, lens[b * KV:(b + 1) * KV], scale)
+    again = run(c, q, kn, vn, None, m, T, lens, kbits, vbits, scale)
+    assert torch.equal(got, again)
+
+
 @pytest.mark.parametrize("n,rep", [(5, 4), (10, 4), (20, 4), (40, 4)])
 def test_scores_that_keep_growing(n, rep):
     """Keys ever longer along the query: every tile passes the running reference, by a little or by a lot."""
@@ -320,3 +343,16 @@ def test_workspace_content_does_not_matter():
     a = run(c, q, kn, vn, None, m, T, None, 0, 4, 0.1, ws=torch.full((size,), 255, dtype=torch.uint8, device=DEV))
     b = run(c, q, kn, vn, None, m, T, None, 0, 4, 0.1, ws=torch.zeros(size, dtype=torch.uint8, device=DEV))
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,rep,T", [(1024, 1, 200), (300, 2, 0), (65, 16, 50)])
+def test_wide_trees(n, rep, T):
+    """Trees of many nodes (several mask words, shared memory beyond the default)."""
+    m = 128
+    c = compress(1, max(T, 1), D, m, 0, 4, 91, False)
+    q, kn, vn = drafted(1, n, 1, rep, 92)
+    mask = random_tree(1, n, 93, empty_row=n // 2)
+    lens = torch.tensor([T], dtype=torch.int32, device=DEV)
+    got = run(c, q, kn, vn, mask, m, max(T, 1), lens, 0, 4, 0.09)
+    kt, vt = vectors(c, 1, max(T, 1), m, 0, 4)
+    check(got, kt, vt, q, kn, vn, mask, lens, 0.09)
