@@ -67,11 +67,15 @@ accumulate_stats_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks)
     }
 }
 
+// Per (chunk, group): a thread holds 4 tokens and adds the queries' weights to them, eight queries' scores in flight.
+// The second read of the scores: the groups are taken in the opposite order, so that those the first kernel read last
+// are still in L2.  VEC: T is a multiple of 4 (16-byte rows); else the 4 tokens are a stride apart.
+template <bool VEC>
 __global__ void __launch_bounds__(kAcThreads)
 accumulate_columns_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks)
 {
-    extern __shared__ float2 rows[];                     // (maximum, 1 / sum) of every row
-    const int64_t g = blockIdx.y;
+    extern __shared__ float4 rows[];                     // maximum, 1 / sum, length in this chunk
+    const int64_t g = gridDim.y - 1 - blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * kAcChunk;
     const float k = a.scale * 1.4426950408889634074f;
@@ -90,22 +94,48 @@ accumulate_columns_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks
             l = l * ac_exp2((m - off) * k) + l2 * ac_exp2((m2 - off) * k);
             m = mn;
         }
-        if (lane == 0) rows[r] = make_float2(m == -INFINITY ? 0.0f : m, l == 0.0f ? 0.0f : 1.0f / l);
+        if (lane == 0) {
+            const int64_t left = ac_row_len(a, g * a.nq + r) - t0;
+            rows[r] = make_float4(m == -INFINITY ? 0.0f : m, l == 0.0f ? 0.0f : 1.0f / l,
+                                  __int_as_float(left < 0 ? 0 : (left < kAcChunk ? (int)left : kAcChunk)), 0.0f);
+        }
     }
     __syncthreads();
-    for (int e = 0; e < kAcChunk / kAcThreads; ++e) {
-        const int64_t t = t0 + e * kAcThreads + threadIdx.x;
-        if (t >= a.T) break;
-        float sum = 0.0f;
-        for (int r = 0; r < a.nq; ++r) {
-            const int64_t row = g * a.nq + r;
-            if (t < ac_row_len(a, row)) {
-                const float2 x = rows[r];
-                sum = __fmaf_rn(ac_exp2((__ldg(a.scores + row * a.T + t) - x.x) * k), x.y, sum);
+    // the thread's tokens e = 0 .. 3: first + e step
+    const int first = VEC ? 4 * threadIdx.x : threadIdx.x, step = VEC ? 1 : kAcThreads;
+    const float *src = a.scores + g * a.nq * a.T + t0 + first;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int r0 = 0; r0 < a.nq; r0 += 8) {
+        float v[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int n = r0 + i < a.nq ? __float_as_int(rows[r0 + i].z) : 0;      // tokens of the chunk that it sees
+            const float *p = src + (int64_t)(r0 + i) * a.T;
+            if (VEC && first + 3 < n) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
+                v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] = first + e * step < n ? __ldg(p + e * step) : -INFINITY;
             }
         }
-        const float old = a.decay == 0.0f ? 0.0f : a.decay * a.acc[g * a.T + t];
-        a.out[g * a.T + t] = old + sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (r0 + i >= a.nq) break;
+            const float4 x = rows[r0 + i];
+            const int n = __float_as_int(x.z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (first + e * step < n) sum[e] = __fmaf_rn(ac_exp2((v[i][e] - x.x) * k), x.y, sum[e]);
+        }
+    }
+    const float *acc = a.acc + g * a.T + t0 + first;
+    float *out = a.out + g * a.T + t0 + first;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (t0 + first + e * step >= a.T) break;
+        out[e * step] = (a.decay == 0.0f ? 0.0f : a.decay * acc[e * step]) + sum[e];
     }
 }
 
@@ -122,8 +152,13 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t st)
     const dim3 grid((unsigned)n_chunks, (unsigned)a.G);
     accumulate_stats_kernel<<<grid, kAcThreads, 0, st>>>(a, n_chunks);
     note_launch("accumulate_stats_kernel");
-    const size_t smem = (size_t)a.nq * sizeof(float2);
-    accumulate_columns_kernel<<<grid, kAcThreads, smem, st>>>(a, n_chunks);
+    const size_t smem = (size_t)a.nq * sizeof(float4);
+    auto columns = a.T % 4 == 0 ? accumulate_columns_kernel<true> : accumulate_columns_kernel<false>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(columns, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    columns<<<grid, kAcThreads, smem, st>>>(a, n_chunks);
     note_launch("accumulate_columns_kernel");
     return cudaGetLastError();
 }
@@ -134,6 +169,7 @@ namespace {
 
 constexpr int kSeThreads = 1024;
 constexpr int kSeMaxCluster = 8;
+constexpr uint32_t kSeCandidates = 128;
 
 // Sort key of a weight sum: larger sums have larger keys, -0 equals +0, NaN comes last (key 1); 0 is "no token".
 __device__ __forceinline__ uint32_t se_key(float x)
@@ -145,9 +181,9 @@ __device__ __forceinline__ uint32_t se_key(float x)
 
 // One cluster per group.  CTA c of the cluster holds the keys of tokens [c slice, (c + 1) slice), IT a thread in
 // registers (IT = 0: read again from global memory in every pass).  The threshold (the keep-th largest key) is found
-// four bits at a time: every thread counts the digits of its keys that still match, counts are summed over the
+// four bits at a time: every warp counts the digits of its keys that still match by ballots, counts are summed over the
 // cluster (integer sums: no order matters), and the digit in which the rank falls is appended; it ends early when
-// all keys that match are wanted.  Then every CTA writes its kept indices at its place in index order.
+// all keys that match are wanted, or few enough match to rank them directly.  Then every CTA writes its kept indices at its place in index order.
 // The search is bound by the latency of its (at most eight) rounds, not by the one read of the sums.
 template <int IT>
 __global__ void __launch_bounds__(kSeThreads, 1)
@@ -161,6 +197,8 @@ select_kernel(const __grid_constant__ SelectArgs a, int64_t slice)
     __shared__ uint32_t all[2][kSeMaxCluster][16];           // every CTA's, written by its owner
     __shared__ uint32_t above[kSeMaxCluster][2];             // every CTA's keys above / at the threshold
     __shared__ uint32_t wpre[32][2];
+    __shared__ uint32_t cand[kSeCandidates];                 // the last keys that match, of all CTAs
+    __shared__ uint32_t found[2], n_cand;
 
     int64_t len = a.T;
     if (a.len) {
@@ -194,6 +232,7 @@ select_kernel(const __grid_constant__ SelectArgs a, int64_t slice)
         }
     };
     if (tid < 32) local[tid >> 4][tid & 15] = 0u;
+    if (tid == 32) n_cand = 0u;
     cl.sync();                                               // every CTA of the cluster has started
 
     uint32_t prefix = 0u, mask = 0u;                         // keys with (key & mask) == prefix still match
@@ -201,28 +240,26 @@ select_kernel(const __grid_constant__ SelectArgs a, int64_t slice)
     bool every = need == 0u || len <= keep;                  // all matching keys (not 0) are wanted
     for (int round = 0; round < 8 && !every; ++round) {
         const int shift = 28 - 4 * round, par = round & 1;
-        uint32_t n[8];                                       // digits 2 i (low half) and 2 i + 1 (high half)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = 0u;
+        uint32_t n = 0u;                                     // lane: the warp's keys with digit lane % 16
         for_keys([&](int, uint32_t kk) {
-            const uint32_t d = (kk >> shift) & 15u;
-            const uint32_t one = (kk != 0u && (kk & mask) == prefix) ? 1u << (16 * (d & 1)) : 0u;
+            const uint32_t d = kk >> shift;
+            uint32_t m = __ballot_sync(0xffffffffu, kk != 0u && (kk & mask) == prefix);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) n[i] += (d >> 1) == (uint32_t)i ? one : 0u;
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t set = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+                m &= (lane >> b) & 1 ? set : ~set;
+            }
+            n += __popc(m);
         });
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = __reduce_add_sync(0xffffffffu, n[i] & 0xffffu), hi = __reduce_add_sync(0xffffffffu, n[i] >> 16);
-            if (lane == 0 && lo) atomicAdd(&local[par][2 * i], lo);
-            if (lane == 1 && hi) atomicAdd(&local[par][2 * i + 1], hi);
-        }
+        if (lane < 16 && n) atomicAdd(&local[par][lane], n);
         __syncthreads();
         if (tid < 16 * C) {
             uint32_t *dst = cl.map_shared_rank(&all[par][rank][tid & 15], tid >> 4);
             *dst = local[par][tid & 15];
         }
         if (tid >= kSeThreads - 16) local[par ^ 1][tid & 15] = 0u;
-        cl.sync();
+        if (C > 1) cl.sync();
+        else __syncthreads();
         uint32_t total = 0u;                                 // lane: digit 15 - lane
         if (lane < 16)
             for (int c = 0; c < C; ++c) total += all[par][c][15 - lane];
@@ -238,6 +275,35 @@ select_kernel(const __grid_constant__ SelectArgs a, int64_t slice)
         prefix |= (uint32_t)(15 - src) << shift;
         mask |= 15u << shift;
         every = in == need;
+        if (!every && in <= kSeCandidates) {
+            // few keys match: every CTA gets all of them (the places are known from the round's counts) and ranks them
+            uint32_t at = 0u;
+            for (int c = 0; c < rank; ++c) at += all[par][c][15 - src];
+            for_keys([&](int, uint32_t kk) {
+                if (kk == 0u || (kk & mask) != prefix) return;
+                const uint32_t i = at + atomicAdd(&n_cand, 1u);
+                for (int c = 0; c < C; ++c) *cl.map_shared_rank(&cand[i], c) = kk;
+            });
+            if (C > 1) cl.sync();
+            else __syncthreads();
+            if (tid < (int)in) {
+                const uint32_t kk = cand[tid];
+                uint32_t above_it = 0u, same = 0u;
+                for (uint32_t i = 0; i < in; ++i) {
+                    above_it += cand[i] > kk;
+                    same += cand[i] == kk;
+                }
+                if (above_it < need && need <= above_it + same) {
+                    found[0] = kk;
+                    found[1] = need - above_it;
+                }
+            }
+            __syncthreads();
+            prefix = found[0];
+            mask = 0xffffffffu;
+            need = found[1];
+            break;
+        }
     }
     // keys above the threshold are kept; of those that match it, the first `need` in index order
     const uint32_t kept = len < keep ? (uint32_t)len : (uint32_t)keep;
@@ -327,36 +393,51 @@ cudaError_t launch_select(const SelectArgs &a, cudaStream_t st)
 namespace {
 
 constexpr int kGaThreads = 256;
-constexpr int kGaRows = 64;
 
+// Four units of a thread in flight.
 template <typename U>
 __device__ __forceinline__ void ga_copy(const uint8_t *src, uint8_t *dst, int units, const int32_t *rows, int n)
 {
     const U *s = reinterpret_cast<const U *>(src);
     U *d = reinterpret_cast<U *>(dst);
-    for (int i = threadIdx.x; i < n * units; i += kGaThreads) {
-        const int r = i / units, u = i - r * units, t = rows[r];
-        if (t >= 0) d[i] = __ldg(s + (int64_t)t * units + u);
+    const int shift = (units & (units - 1)) == 0 ? 31 - __clz(units) : -1;
+    for (int i0 = threadIdx.x; i0 < n * units; i0 += 4 * kGaThreads) {
+        U v[4];
+        bool take[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e * kGaThreads;
+            take[e] = i < n * units;
+            if (!take[e]) continue;
+            const int r = shift >= 0 ? i >> shift : i / units, u = i - r * units, t = rows[r];
+            take[e] = t >= 0;
+            if (take[e]) v[e] = __ldg(s + (int64_t)t * units + u);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (take[e]) d[i0 + e * kGaThreads] = v[e];
     }
 }
 
-// A CTA moves kGaRows kept rows of one group in every array, in the widest unit that divides the row.
+// A CTA moves ROWS kept rows of one group in one array (blockIdx.z), in the widest unit that divides the row.
+template <int ROWS>
 __global__ void __launch_bounds__(kGaThreads)
 gather_kernel(const __grid_constant__ GatherArgs a)
 {
-    __shared__ int32_t rows[kGaRows];
+    __shared__ int32_t rows[ROWS];
     const int64_t g = blockIdx.y;
-    const int j0 = blockIdx.x * kGaRows;
+    const int j0 = blockIdx.x * ROWS;
     int n = __ldg(a.count + g);
     n = n < a.keep ? n : a.keep;
-    n = n - j0 < kGaRows ? n - j0 : kGaRows;
+    n = n - j0 < ROWS ? n - j0 : ROWS;
     if (n <= 0) return;
-    if (threadIdx.x < n) {
-        const int t = __ldg(a.idx + g * a.keep + j0 + threadIdx.x);
-        rows[threadIdx.x] = t >= 0 && t < a.T ? t : -1;      // an index outside the cache moves nothing
+    for (int i = threadIdx.x; i < n; i += kGaThreads) {
+        const int t = __ldg(a.idx + g * a.keep + j0 + i);
+        rows[i] = t >= 0 && t < a.T ? t : -1;                // an index outside the cache moves nothing
     }
     __syncthreads();
-    for (int k = 0; k < a.n_arrays; ++k) {
+    {
+        const int k = blockIdx.z;
         const int64_t rb = a.row_bytes[k];
         const uint8_t *src = a.src[k] + g * a.T * rb;
         uint8_t *dst = a.dst[k] + (g * a.T_dst + j0) * rb;
@@ -373,8 +454,12 @@ gather_kernel(const __grid_constant__ GatherArgs a)
 
 cudaError_t launch_gather(const GatherArgs &a, cudaStream_t st)
 {
-    const dim3 grid((unsigned)((a.keep + kGaRows - 1) / kGaRows), (unsigned)a.G);
-    gather_kernel<<<grid, kGaThreads, 0, st>>>(a);
+    // rows a CTA: enough to keep its threads' loads in flight, unless that leaves SMs without work
+    const bool wide = (int64_t)a.keep * a.G >= 256 * 512;
+    const int rows = wide ? 256 : 64;
+    const dim3 grid((unsigned)((a.keep + rows - 1) / rows), (unsigned)a.G, (unsigned)a.n_arrays);
+    if (wide) gather_kernel<256><<<grid, kGaThreads, 0, st>>>(a);
+    else gather_kernel<64><<<grid, kGaThreads, 0, st>>>(a);
     note_launch("gather_kernel");
     return cudaGetLastError();
 }

@@ -125,43 +125,55 @@ rotary_kernel(const __grid_constant__ RotaryArgs a)
     }
     const int n_all = a.n_heads + a.n_heads2;
     const int h_end = min(n_all, ((int)blockIdx.y + 1) * a.heads_per_block);
-    for (int h = blockIdx.y * a.heads_per_block + h0; h < h_end; h += a.hs) {
-        const bool second = h >= a.n_heads;
-        const RotaryTensor &T = second ? a.x2 : a.x;
-        const int hh = second ? h - a.n_heads : h;
-        const uint16_t *in = T.in + b * T.in_batch + t * T.in_token + hh * T.in_head;
-        uint16_t *out = T.out + b * T.out_batch + t * T.out_token + hh * T.out_head;
-        const RoVec<V> v0 = ro_load<V>(in + o0);
-        RoVec<V> v1 = v0;
-        if (two) v1 = ro_load<V>(in + o1);
-        if (!rotate) {
-            ro_store<V>(out + o0, v0);
-            if (two) ro_store<V>(out + o1, v1);
-            continue;
+    const int64_t ib = b * a.x.in_batch + t * a.x.in_token, ob = b * a.x.out_batch + t * a.x.out_token;
+    const int64_t ib2 = b * a.x2.in_batch + t * a.x2.in_token, ob2 = b * a.x2.out_batch + t * a.x2.out_token;
+    constexpr int U = 5;                                // heads in flight
+    for (int hb = blockIdx.y * a.heads_per_block + h0; hb < h_end; hb += U * a.hs) {
+        RoVec<V> v0[U], v1[U];
+        uint16_t *out[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = hb + k * a.hs;
+            if (h >= h_end) break;
+            const bool second = h >= a.n_heads;
+            const int hh = second ? h - a.n_heads : h;
+            const uint16_t *in = second ? a.x2.in + ib2 + hh * a.x2.in_head : a.x.in + ib + hh * a.x.in_head;
+            out[k] = second ? a.x2.out + ob2 + hh * a.x2.out_head : a.x.out + ob + hh * a.x.out_head;
+            v0[k] = ro_load<V>(in + o0);
+            if (two) v1[k] = ro_load<V>(in + o1);
         }
-        float p[V], q[V], u[V], w[V];
-        ro_unpack<V, BF16>(v0, p);
-        ro_unpack<V, BF16>(v1, q);
-        if constexpr (HALF) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                u[e] = __fmaf_rn(p[e], c[e], -(q[e] * s[e]));
-                w[e] = __fmaf_rn(q[e], c[e], p[e] * s[e]);
+        for (int k = 0; k < U; ++k) {
+            if (hb + k * a.hs >= h_end) break;
+            if (!rotate) {
+                ro_store<V>(out[k] + o0, v0[k]);
+                if (two) ro_store<V>(out[k] + o1, v1[k]);
+                continue;
             }
-        } else {                                        // values 2e, 2e + 1 of the 2 V in (p, q)
-            float z[2 * V], y[2 * V];
+            float p[V], q[V], u[V], w[V];
+            ro_unpack<V, BF16>(v0[k], p);
+            ro_unpack<V, BF16>(v1[k], q);
+            if constexpr (HALF) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) { z[e] = p[e]; z[V + e] = q[e]; }
+                for (int e = 0; e < V; ++e) {
+                    u[e] = __fmaf_rn(p[e], c[e], -(q[e] * s[e]));
+                    w[e] = __fmaf_rn(q[e], c[e], p[e] * s[e]);
+                }
+            } else {                                    // values 2e, 2e + 1 of the 2 V in (p, q)
+                float z[2 * V], y[2 * V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                y[2 * e] = __fmaf_rn(z[2 * e], c[e], -(z[2 * e + 1] * s[e]));
-                y[2 * e + 1] = __fmaf_rn(z[2 * e + 1], c[e], z[2 * e] * s[e]);
+                for (int e = 0; e < V; ++e) { z[e] = p[e]; z[V + e] = q[e]; }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    y[2 * e] = __fmaf_rn(z[2 * e], c[e], -(z[2 * e + 1] * s[e]));
+                    y[2 * e + 1] = __fmaf_rn(z[2 * e + 1], c[e], z[2 * e] * s[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) { u[e] = y[e]; w[e] = y[V + e]; }
             }
-#pragma unroll
-            for (int e = 0; e < V; ++e) { u[e] = y[e]; w[e] = y[V + e]; }
+            ro_store<V>(out[k] + o0, ro_pack<V, BF16>(u));
+            ro_store<V>(out[k] + o1, ro_pack<V, BF16>(w));
         }
-        ro_store<V>(out + o0, ro_pack<V, BF16>(u));
-        ro_store<V>(out + o1, ro_pack<V, BF16>(w));
     }
 }
 
