@@ -35,7 +35,7 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int NB, bool TWO>
+template <int NB, bool TWO, bool V4>
 cudaError_t launch_main(const TreeArgs &a, const QuantTables &tk, const QuantTables &tv, int grid, cudaStream_t st)
 {
     // weight and value buffers: two of each if the SM's shared memory holds them for tr_ctas CTAs, the values go first
@@ -45,7 +45,7 @@ cudaError_t launch_main(const TreeArgs &a, const QuantTables &tk, const QuantTab
         for (const auto &c : cfg) {
             const size_t smem = tr_smem(NB, a.kb, a.pw, a.vpw, c[0], c[1]);
             if (smem > limit) continue;
-            auto kern = tree_attention_kernel<NB, TWO>;
+            auto kern = tree_attention_kernel<NB, TWO, V4>;
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
             e = launch_early(kern, dim3((unsigned)grid), tr_threads(NB), smem, st, a, tk, tv, c[0], c[1]);
@@ -59,7 +59,8 @@ cudaError_t launch_main(const TreeArgs &a, const QuantTables &tk, const QuantTab
 template <int NB>
 cudaError_t launch_nb(const TreeArgs &a, const QuantTables &tk, const QuantTables &tv, int grid, cudaStream_t st)
 {
-    return a.pw ? launch_main<NB, true>(a, tk, tv, grid, st) : launch_main<NB, false>(a, tk, tv, grid, st);
+    if (a.vpw == 4) return a.pw ? launch_main<NB, true, true>(a, tk, tv, grid, st) : launch_main<NB, false, true>(a, tk, tv, grid, st);
+    return a.pw ? launch_main<NB, true, false>(a, tk, tv, grid, st) : launch_main<NB, false, false>(a, tk, tv, grid, st);
 }
 
 struct Plan {

@@ -41,10 +41,12 @@ constexpr float kTrMost = 15.0f;                  // largest exponent an fp16 we
 
 constexpr int kTrAhead = 4;                       // tiles that the cache's records are prefetched into L2 ahead
 
-// Warps of a CTA: NB / 32 groups of four softmax warps (a group has 32 rows), two groups of four producer warps (a
-// group unpacks every second tile), two issuing warps.
+// Warps of a CTA: NB / 32 groups of four softmax warps (a group has 32 rows), groups of four producer warps (with two,
+// a group unpacks every second tile), two issuing warps.  Measured at 32 rows: one producer group in each of two CTAs
+// an SM 137 us, two groups 146 us (spills at 72 registers), one CTA 197 us; at 128: one group 476 us, two 494 us; at 64
+// two groups 52 us, one 62 us.
 __host__ __device__ constexpr int tr_softmax_warps(int nb) { return nb / 8; }
-__host__ __device__ constexpr int tr_producer_groups(int) { return 2; }
+__host__ __device__ constexpr int tr_producer_groups(int nb) { return nb == 64 ? 2 : 1; }
 __host__ __device__ constexpr int tr_threads(int nb) { return (tr_softmax_warps(nb) + 4 * tr_producer_groups(nb) + 2) * 32; }
 __host__ __device__ constexpr int tr_ctas(int nb) { return nb == 32 ? 2 : 1; }
 // TMEM: score buffers, O, the weight sums (16 columns), key slots of 32 columns
@@ -334,7 +336,9 @@ __device__ __forceinline__ void tr_load_codes(const uint8_t *p, int pw, bool val
     }
 }
 
-template <int NB, bool TWO>
+// V4: values of 4 bits (fewer and wider loads, no choice of width in the loop: 137 -> 124 us at 32 rows x 32 x 32768
+// tokens, 476 -> 458 us at 256 rows).
+template <int NB, bool TWO, bool V4>
 __global__ void __launch_bounds__(tr_threads(NB), tr_ctas(NB))
 tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ QuantTables TK,
                       const __grid_constant__ QuantTables TV, int np, int nv)
@@ -509,7 +513,19 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             }
             uint32_t vc[16];
             const uint16_t hv = valid ? __ldg(a.vnorms + row) : (uint16_t)0;
-            tr_load_codes<0, 4>(a.vcodes + row * vbytes, a.vpw, valid, vc);
+            auto load_values = [&](int half) {
+                if constexpr (V4) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.vcodes + row * 64) + 2 * half;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 x = valid ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+                        vc[4 * i] = x.x; vc[4 * i + 1] = x.y; vc[4 * i + 2] = x.z; vc[4 * i + 3] = x.w;
+                    }
+                } else {
+                    tr_load_codes<0, 4>(a.vcodes + row * vbytes + half * 8 * a.vpw, a.vpw, valid, vc);
+                }
+            };
+            load_values(0);
             advance(it, c);
             if (c + NPG < count) {
                 load_signs(it, 0);
@@ -522,7 +538,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             uint32_t Vr = sV0 + (uint32_t)vb * kTrVBytes + (uint32_t)r * 128u;
 #pragma unroll 1
             for (int half = 0; half < 2; ++half, Vr += kTrVBytes / 2) {
-                if (a.vpw > 4) tr_load_codes<4, 8>(a.vcodes + row * vbytes + half * 8 * a.vpw, a.vpw, valid, vc);
+                if (!V4 && a.vpw > 4) tr_load_codes<4, 8>(a.vcodes + row * vbytes + half * 8 * a.vpw, a.vpw, valid, vc);
                 if (half == 0 && c >= nv && ok && !pv_wait(c - nv)) ok = false;  // the tile whose values lie here.  With a
                 // barrier for every fourth tile the phase before this one has been waited for (at this group's last
                 // tile) and the next one needs this tile's values, so the parity tells.
@@ -539,10 +555,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                     }
                 };
                 uint32_t o[16];
-                tr_lookup_any<VCL, 0, 16>(a.vpw, vc, vlut0, lane4v, o);
+                if constexpr (V4) tr_lookup<4, VCL, 0, 16>(vc, vlut0, lane4v, o);
+                else tr_lookup_any<VCL, 0, 16>(a.vpw, vc, vlut0, lane4v, o);
                 store(0, o);
-                tr_lookup_any<VCL, 16, 16>(a.vpw, vc, vlut0, lane4v, o);
-                if (half == 0) tr_load_codes<0, 4>(a.vcodes + row * vbytes + 8 * a.vpw, a.vpw, valid, vc);
+                if constexpr (V4) tr_lookup<4, VCL, 16, 16>(vc, vlut0, lane4v, o);
+                else tr_lookup_any<VCL, 16, 16>(a.vpw, vc, vlut0, lane4v, o);
+                if (half == 0) load_values(1);
                 store(4, o);
             }
             fence_proxy_async_smem();

@@ -1023,9 +1023,9 @@ rq_status rq_rotary(const void *x, const rq_strides *x_strides, void *out, const
     if (a.num_sms <= 0) return RQ_ECUDA;
     for (int i = 0; i < rot_dim / 2; ++i) {
         // freq / 2 pi modulo 1 in 0.64 fixed point (80-bit long double: 64 significant bits)
-        const long double turn = (long double)freq[i] / 6.283185307179586476925286766559005768L;
-        const long double frac = turn - floorl(turn);
-        const long double fixed = frac * 18446744073709551616.0L;
+        const long double turn = (long double)freq[i] * 0.159154943091895335768883763372514362L;
+        const int64_t whole = (int64_t)turn - (turn < 0.0L ? 1 : 0);        // |turn| < 2^18
+        const long double fixed = (turn - (long double)whole) * 18446744073709551616.0L;
         a.turns[i] = fixed >= 18446744073709551615.0L ? 0ull : (uint64_t)(fixed + 0.5L);
     }
     return cuda_status(rq::launch_rotary(a, reinterpret_cast<cudaStream_t>(stream)));
