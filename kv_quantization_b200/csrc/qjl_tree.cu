@@ -38,7 +38,8 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem
 template <int NB, bool TWO, bool V4>
 cudaError_t launch_main(const TreeArgs &a, const QuantTables &tk, const QuantTables &tv, int grid, cudaStream_t st)
 {
-    // weight and value buffers: two of each if the SM's shared memory holds them for tr_ctas CTAs, the values go first
+    // weight and value buffers: two of each if the SM's shared memory holds them for tr_ctas CTAs (one weight buffer and
+    // two value buffers, or the other way round, measured the same); else one CTA an SM
     const int cfg[][2] = {{2, 2}, {1, 2}, {1, 1}};
     const size_t limits[] = {kMaxSmemPerBlock / tr_ctas(NB) - 1024 * (tr_ctas(NB) - 1), kMaxSmemPerBlock};
     for (const size_t limit : limits) {

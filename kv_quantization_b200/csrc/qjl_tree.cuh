@@ -16,16 +16,21 @@
 // Main kernel, per 128-token tile and block of NB query rows.  Tokens are the M dimension of the score product
 // (S^T = K . Q^T, one token a TMEM lane), so that every lane works however few rows there are, and a thread's
 // token-wise factors are its own registers:
-//   producers (8 warps)  thread = token and half of its slices: 64 key values a slice are unpacked to fp16 and stored
-//                        to TMEM, where the score product reads its A operand: unpacked keys never pass through
-//                        shared memory, whose bandwidth bounds this kernel otherwise.  Then half the token's values,
-//                        V' = fp16(c) * fp16(n / d), to shared memory.
+//   producers (groups of 4 warps)  thread = token: 64 key values a slice are unpacked to fp16 and stored to TMEM, where
+//                        the score product reads its A operand: unpacked keys never pass through shared memory.  Then
+//                        the token's values, V' = fp16(c) * fp16(n / d), to shared memory.
 //   MMA 1 (one thread)   S^T[token][row] += K slice (TMEM) . Q^T slice (shared memory).
-//   softmax (4 or 8 warps) thread = token, rows in chunks of 32: p = 2^(s g cq + (8 - ref)), fp16 P to shared memory.
-//                        The reference `ref` of a row is the maximum of the segment's first tile and moves only when a
-//                        score passes it by 7 (2^15 is the most fp16 weights take): the usual tile needs one vote
-//                        and no reduction over tokens.
-//   MMA 2 (one thread)   O^T[d][row] += V'^T . P, accumulated in TMEM over the segment.
+//   softmax (4 warps for 32 rows)  thread = token: weights 2^((s - Q) g + 8 - ref), fp16, to shared memory.  The reference
+//                        `ref` of a row is the maximum of the segment's first tile and moves only when a score passes
+//                        it by 7 (2^15 is the most fp16 weights take): the usual tile needs one vote, taken while the
+//                        weights are computed, and no reduction over tokens.
+//   MMA 2 (one thread)   O^T[d][row] += V'^T . P and the rows' weight sums P^T . 1, in TMEM over the segment.
+//
+// Measured (B200): 32 rows x 32 groups x 32768 tokens, m = 256, 4-bit values: 113 us whole (105 MB: 16 us at the copy
+// rate; 26 GFLOP of score and value products: 16 us); 256 rows: 452 us (206 GFLOP: 125 us).  What bounds it: neither
+// memory (DRAM 8 %) nor the tensor pipe (10 and 27 %), but the instructions around them, about 7600 a 128-token tile of
+// 32 rows at 0.4 issued per scheduler and cycle: unpacking (1800), weights (900), and the waits, address arithmetic and
+// barriers of the roles.
 #pragma once
 #include "rq_cache_ops.h"
 #include "rq_common.cuh"
@@ -53,9 +58,10 @@ __host__ __device__ constexpr int tr_ctas(int nb) { return nb == 32 ? 2 : 1; }
 __host__ __device__ constexpr int tr_sbufs(int nb) { return nb == 128 ? 1 : 2; }
 __host__ __device__ constexpr int tr_kslots(int nb) { return nb == 32 ? 4 : nb == 64 ? 8 : 6; }
 __host__ __device__ constexpr int tr_tmem(int nb) { return nb == 32 ? 256 : 512; }
-// log2 of the copies of the value and key lookup tables (more copies: fewer bank conflicts)
-__host__ __device__ constexpr int tr_vcl(int nb) { return nb == 32 ? 3 : 4; }
-__host__ __device__ constexpr int tr_kcl(int nb) { return nb == 64 ? 4 : 3; }
+// log2 of the copies of the value and key lookup tables: 32 copies have no bank conflicts (values with 8: 124 us, 16: 118,
+// 32: 113 at 32 rows); the keys' have fewer where shared memory is short.
+__host__ __device__ constexpr int tr_vcl(int) { return 5; }
+__host__ __device__ constexpr int tr_kcl(int nb) { return nb == 64 ? 5 : 3; }
 __host__ __device__ inline size_t tr_pbytes(int nb) { return (size_t)(nb > 64 ? 2 : 1) * kTrTok * 128; }
 __host__ __device__ inline size_t tr_lut_bytes(int pw, int cl)
 {
@@ -447,6 +453,16 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         auto load_signs = [&](const TreeIter &p, int first) {
             const uint2 *src = reinterpret_cast<const uint2 *>(a.signs + (p.row + r) * sbytes) + first;
             const bool valid = r < p.left;
+            if (a.m % 128 == 0) {                               // rows of whole 16 bytes
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (first + i < nsig && valid) x = __ldg(reinterpret_cast<const uint4 *>(src + i));
+                    sg[i] = make_uint2(x.x, x.y);
+                    sg[i + 1] = make_uint2(x.z, x.w);
+                }
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sg[i] = make_uint2(0u, 0u);
