@@ -436,7 +436,8 @@ typedef struct { const void *src; void *dst; int64_t row_bytes; } rq_rows;
  * of every array (HOST array of 1 .. 16 rq_rows: codes, norms, sign bits, sums)
  * to rows 0 .. count[g] - 1 of dst; rows behind them are left as they were, and
  * so is the row of an index outside 0 .. T-1.  T_dst >= keep; row_bytes 1 ..
- * 65536; src and dst of an array must not overlap (RQ_EINVAL). */
+ * 65536; no dst may overlap any src
+ * or another dst (RQ_EINVAL). */
 rq_status rq_evict_gather(const int32_t *idx, const int32_t *count, int64_t G, int keep, int64_t T, int64_t T_dst,
                           const rq_rows *arrays, int n_arrays, rq_stream_t stream);
 

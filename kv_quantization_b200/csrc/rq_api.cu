@@ -1093,9 +1093,14 @@ rq_status rq_evict_gather(const int32_t *idx, const int32_t *count, int64_t G, i
         const rq_rows &r = arrays[i];
         if (!r.src || !r.dst) return RQ_EINVAL;
         if (!aligned16(r.src) || !aligned16(r.dst)) return RQ_EALIGN;
-        const uintptr_t s0 = reinterpret_cast<uintptr_t>(r.src), d0 = reinterpret_cast<uintptr_t>(r.dst);
-        const uintptr_t sn = (uintptr_t)G * T * r.row_bytes, dn = (uintptr_t)G * T_dst * r.row_bytes;
-        if (s0 < d0 + dn && d0 < s0 + sn) return RQ_EINVAL;
+        // what one array's rows are moved to must not be read or written for another
+        const uintptr_t d0 = reinterpret_cast<uintptr_t>(r.dst), dn = (uintptr_t)G * T_dst * r.row_bytes;
+        for (int j = 0; j < n_arrays; ++j) {
+            const uintptr_t s0 = reinterpret_cast<uintptr_t>(arrays[j].src), sn = (uintptr_t)G * T * arrays[j].row_bytes;
+            const uintptr_t e0 = reinterpret_cast<uintptr_t>(arrays[j].dst), en = (uintptr_t)G * T_dst * arrays[j].row_bytes;
+            if (s0 < d0 + dn && d0 < s0 + sn) return RQ_EINVAL;
+            if (j != i && e0 < d0 + dn && d0 < e0 + en) return RQ_EINVAL;
+        }
         a.src[i] = static_cast<const uint8_t *>(r.src);
         a.dst[i] = static_cast<uint8_t *>(r.dst);
         a.row_bytes[i] = r.row_bytes;

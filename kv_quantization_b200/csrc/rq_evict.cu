@@ -33,7 +33,9 @@ __device__ __forceinline__ int64_t ac_row_len(const AccumulateArgs &a, int64_t r
     return n < 0 ? 0 : (n < a.T ? n : a.T);
 }
 
-// Per (row, chunk): maximum and sum of exponentials.  A warp takes a row of the chunk.
+// Per (row, chunk): maximum and sum of exponentials.  A warp takes a row of the chunk; VEC: T is a multiple of 4, and a
+// lane's values are 4 neighbours.  Bound by the read of the scores.
+template <bool VEC>
 __global__ void __launch_bounds__(kAcThreads)
 accumulate_stats_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks)
 {
@@ -47,10 +49,18 @@ accumulate_stats_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks)
         const int n = left < 0 ? 0 : (left < kAcChunk ? (int)left : kAcChunk);
         const float *s = a.scores + row * a.T + t0;
         float v[kAcChunk / 32], m = -INFINITY;
+        if (VEC && n == kAcChunk) {
 #pragma unroll
-        for (int j = 0; j < kAcChunk / 32; ++j) {
-            const int t = j * 32 + lane;
-            v[j] = t < n ? __ldg(s + t) : -INFINITY;
+            for (int j = 0; j < kAcChunk / 32; j += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(s) + (j / 4) * 32 + lane);
+                v[j] = x.x; v[j + 1] = x.y; v[j + 2] = x.z; v[j + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kAcChunk / 32; ++j) {
+                const int t = j * 32 + lane;
+                v[j] = t < n ? __ldg(s + t) : -INFINITY;
+            }
         }
 #pragma unroll
         for (int j = 0; j < kAcChunk / 32; ++j) m = fmaxf(m, v[j]);
@@ -58,7 +68,8 @@ accumulate_stats_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks)
         const float off = m == -INFINITY ? 0.0f : m;
         float l = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kAcChunk / 32; ++j) l += j * 32 + lane < n ? ac_exp2((v[j] - off) * k) : 0.0f;
+        for (int j = 0; j < kAcChunk / 32; ++j)          // (a whole chunk has no places behind its row's length)
+            l += n == kAcChunk || j * 32 + lane < n ? ac_exp2((v[j] - off) * k) : 0.0f;
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         if (lane == 0) {
             float2 *p = reinterpret_cast<float2 *>(a.workspace) + row * n_chunks + blockIdx.x;
@@ -150,7 +161,8 @@ cudaError_t launch_accumulate(const AccumulateArgs &a, cudaStream_t st)
 {
     const int n_chunks = (int)((a.T + kAcChunk - 1) / kAcChunk);
     const dim3 grid((unsigned)n_chunks, (unsigned)a.G);
-    accumulate_stats_kernel<<<grid, kAcThreads, 0, st>>>(a, n_chunks);
+    if (a.T % 4 == 0) accumulate_stats_kernel<true><<<grid, kAcThreads, 0, st>>>(a, n_chunks);
+    else accumulate_stats_kernel<false><<<grid, kAcThreads, 0, st>>>(a, n_chunks);
     note_launch("accumulate_stats_kernel");
     const size_t smem = (size_t)a.nq * sizeof(float4);
     auto columns = a.T % 4 == 0 ? accumulate_columns_kernel<true> : accumulate_columns_kernel<false>;
@@ -183,7 +195,8 @@ __device__ __forceinline__ uint32_t se_key(float x)
 // registers (IT = 0: read again from global memory in every pass).  The threshold (the keep-th largest key) is found
 // four bits at a time: every warp counts the digits of its keys that still match by ballots, counts are summed over the
 // cluster (integer sums: no order matters), and the digit in which the rank falls is appended; it ends early when
-// all keys that match are wanted, or few enough match to rank them directly.  Then every CTA writes its kept indices at its place in index order.
+// all keys that match are wanted, or few enough match to rank them directly.  Then every CTA writes its kept indices at
+// its place in index order.
 // The search is bound by the latency of its (at most eight) rounds, not by the one read of the sums.
 template <int IT>
 __global__ void __launch_bounds__(kSeThreads, 1)

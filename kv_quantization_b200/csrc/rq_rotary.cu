@@ -189,7 +189,7 @@ cudaError_t ro_launch(RotaryArgs a, cudaStream_t st)
     if (a.hs > slots) a.hs = slots;
     a.tb = slots / a.hs;
     a.heads_per_block = heads;
-    if (a.tb == 1 && a.hs == slots && tokens < 2 * a.num_sms) a.heads_per_block = a.hs;
+    if (a.tb == 1 && a.hs == slots && tokens < 2 * a.num_sms && heads / a.hs < 65535) a.heads_per_block = a.hs;
     if (a.tb > 1 && tokens < 2 * a.num_sms) a.tb = 1;
     const int64_t gx = (tokens + a.tb - 1) / a.tb;
     if (gx > 0x7fffffff) return cudaErrorInvalidValue;

@@ -165,6 +165,16 @@ def test_gather_refuses(kw, status):
                                    a["n"], None) == status
 
 
+def test_gather_refuses_arrays_that_share_memory():
+    rows = (L.Rows * 2)()
+    for r, src, dst in zip(rows, (A, A + 0x10000), (A + 0x20000, A + 0x20080)):
+        r.src, r.dst, r.row_bytes = src, dst, 16
+    call = lambda: L.lib().rq_evict_gather(A, A, 2, 8, 20, 8, C.addressof(rows), 2, None)  # noqa: E731
+    assert call() == EINVAL                                    # two destinations
+    rows[1].dst = A
+    assert call() == EINVAL                                    # a destination and another array's source
+
+
 def test_gather_binding_checks_sizes():
     src, dst = torch.zeros(2, 20, 3), torch.zeros(2, 7, 3)
     with pytest.raises(ValueError):
