@@ -7,8 +7,8 @@ namespace {
 
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
-// Query rows a block: 32 or 64 when that holds the group's rows; above, 128 (fewer passes over the cache, twice the
-// products per unpacked key) where the operand of kb columns leaves room for two weight buffers in shared memory.
+// Query rows a block: 32 or 64 when that holds the group's rows; above, 128 (fewer passes over the cache: 256 rows in
+// blocks of 128 397 us, of 64 482 us, of 32 732 us) where the operand of kb columns leaves room in shared memory.
 int tree_nb(int rows, int kb) { return rows <= 32 ? 32 : (rows <= 64 || kb > 384 ? 64 : 128); }
 
 int64_t tree_grid(int64_t G, int rbs, int nb, int64_t T, int num_sms)

@@ -27,9 +27,9 @@
 //   MMA 2 (one thread)   O^T[d][row] += V'^T . P and the rows' weight sums P^T . 1, in TMEM over the segment.
 //
 // Measured (B200): 32 rows x 32 groups x 32768 tokens, m = 256, 4-bit values: 113 us whole (105 MB: 16 us at the copy
-// rate; 26 GFLOP of score and value products: 16 us); 256 rows: 452 us (206 GFLOP: 125 us).  What bounds it: neither
-// memory (DRAM 8 %) nor the tensor pipe (10 and 27 %), but the instructions around them, about 7600 a 128-token tile of
-// 32 rows at 0.4 issued per scheduler and cycle: unpacking (1800), weights (900), and the waits, address arithmetic and
+// rate; 26 GFLOP of score and value products: 16 us); 256 rows: 397 us (206 GFLOP: 125 us).  What bounds it: neither
+// memory (DRAM 8 %) nor the tensor pipe (11 and 24 %), but the instructions around them, about 7000 a 128-token tile of
+// 32 rows at 0.44 issued per scheduler and cycle: unpacking (1800), weights (900), and the waits, address arithmetic and
 // barriers of the roles.
 #pragma once
 #include "rq_cache_ops.h"
@@ -716,24 +716,27 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             if (ok && !mbar_wait(&s_full[c & 1], (uint32_t)((c >> 1) & 1))) ok = false;
             tc_fence_after();
             uint32_t sr[32], w[16];                             // scores, then exponents; fp16 weights of row pairs
-            tmem_ld32(tS + (uint32_t)(c % NS * NB + cb) + lanes, sr);
-            tmem_ld_wait();
-            tc_fence_before();                                  // the scores are read
-            __syncwarp();
-            if (lane == 0) tr_arrive(&s_empty[c & 1]);
-            // exponents (s - Q) gg + (8 - ref) (at the start of a segment: before any reference) and their maximum
-            float mx = -INFINITY;
+            // Exponents (s - Q) gg + (8 - ref) (at the start of a segment: before any reference) and their maximum.  The
+            // scores stay in TMEM until the vote is known: held in registers for the unusual answer they spill (256 rows:
+            // 444 us instead of 397).
+            auto exponents = [&]() {
+                tmem_ld32(tS + (uint32_t)(c % NS * NB + cb) + lanes, sr);
+                tmem_ld_wait();
+                float mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const float4 f = tr_lds_f4(sF0 + (uint32_t)j * 8u);
-                const float2 off = TWO ? make_float2(f.z, f.w)
-                                       : __ffma2_rn(make_float2(f.x, f.y), make_float2(gg, gg), make_float2(f.z, f.w));
-                const float2 v = __ffma2_rn(make_float2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])),
-                                            make_float2(gg, gg), off);
-                sr[j] = __float_as_uint(v.x);
-                sr[j + 1] = __float_as_uint(v.y);
-                mx = fmaxf(fmaxf(mx, v.x), v.y);
-            }
+                for (int j = 0; j < 32; j += 2) {
+                    const float4 f = tr_lds_f4(sF0 + (uint32_t)j * 8u);
+                    const float2 off = TWO ? make_float2(f.z, f.w)
+                                           : __ffma2_rn(make_float2(f.x, f.y), make_float2(gg, gg), make_float2(f.z, f.w));
+                    const float2 v = __ffma2_rn(make_float2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])),
+                                                make_float2(gg, gg), off);
+                    sr[j] = __float_as_uint(v.x);
+                    sr[j + 1] = __float_as_uint(v.y);
+                    mx = fmaxf(fmaxf(mx, v.x), v.y);
+                }
+                return mx;
+            };
+            const float mx = exponents();
             auto weights = [&]() {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -756,6 +759,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             if (slow) {
                 // new references: the maxima over the tile's tokens
                 uint32_t t[32];
+                exponents();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) t[j] = valid ? sr[j] : 0xff800000u;
                 sX[quarter * NB + cb + lane] = tr_reduce_columns(t, lane, [](float p, float q) { return fmaxf(p, q); });
@@ -792,6 +796,9 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                     tc_fence_before();
                 }
             }
+            tc_fence_before();                                  // the scores are read
+            __syncwarp();
+            if (lane == 0) tr_arrive(&s_empty[c & 1]);
             if (c >= np && ok && !pv_wait(c - np)) ok = false;  // the tile whose weights lie in the buffer
             // row r of the [token][row] operand
             const uint32_t Pr = sP0 + (np == 2 ? (uint32_t)(c & 1) * (uint32_t)tr_pbytes(NB) : 0u) +
