@@ -210,11 +210,12 @@ cudaError_t ro_launch(RotaryArgs a, cudaStream_t st)
 
 cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t st)
 {
-    // the widest vector that divides the pairs, the copied tail and every stride (base pointers are 16-byte aligned)
+    // the widest vector that divides the pairs, the copied tail, every stride and every base address
     int64_t all = (int64_t)(a.rot / 2) | (a.d - a.rot);
     for (const RotaryTensor *t : {&a.x, &a.x2}) {
         if (t->in == nullptr) continue;
         all |= t->in_batch | t->in_token | t->in_head | t->out_batch | t->out_token | t->out_head;
+        all |= (int64_t)((reinterpret_cast<uintptr_t>(t->in) | reinterpret_cast<uintptr_t>(t->out)) / sizeof(uint16_t));
     }
     if (all % 8 == 0) return ro_launch<8>(a, st);
     if (all % 4 == 0) return ro_launch<4>(a, st);

@@ -112,7 +112,7 @@ def test_odd_strides_and_alignment():
     freq, _ = L.rq_rotary_frequencies(32)
     want = torch.empty_like(x)
     L.rq_rotary(x, want, pos, freq, 32, L.RQ_ROPE_HALF)
-    for pad, off in ((4, 4), (2, 2), (1, 1), (3, 0)):
+    for pad, off in ((4, 4), (2, 2), (1, 1), (3, 0), (8, 4), (8, 2), (8, 1)):
         buf = torch.zeros(2, 9, 4, 64 + pad, device=DEV, dtype=torch.float16)
         v = buf[..., off:off + 64]
         v.copy_(x)
