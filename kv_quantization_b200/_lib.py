@@ -312,9 +312,9 @@ def _call(name, t, stream, args):
         status = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
     else:
         import torch
-        index = t.device.index
-        raw = torch.cuda.current_stream(index).cuda_stream
-        if index is None or index == torch.cuda.current_device():
+        index, current = t.get_device(), torch._C._cuda_getDevice()
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        if index == current:
             status = fn(*args, raw)
         else:
             with torch.cuda.device(index):
@@ -335,10 +335,10 @@ def _strides(t, what):
 
 
 def _host(a, dtype):
-    """A contiguous host array of dtype (the array itself where it is one)."""
-    if type(a) is np.ndarray and a.dtype == dtype and a.flags.c_contiguous:
-        return a
-    return np.ascontiguousarray(np.asarray(a, dtype=dtype))
+    """The bytes of a host array as dtype."""
+    if type(a) is not np.ndarray or a.dtype != dtype:
+        a = np.asarray(a, dtype=dtype)
+    return a.tobytes()
 
 
 def rq_rotary_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = RQ_ROPE_PLAIN, factor: float = 1.0,
@@ -358,7 +358,7 @@ def rq_rotary(x, out, positions, freq, rot_dim, style, scale=1.0, inverse=False,
     shape = x.shape
     B, n, H, d = shape
     ps = positions.stride()
-    if f.size < rot_dim // 2 or out.shape != shape or positions.dtype != torch.int64 or positions.shape != (B, n) or \
+    if len(f) < rot_dim // 2 * 8 or out.shape != shape or positions.dtype != torch.int64 or positions.shape != (B, n) or \
             (n > 1 and ps[1] != 1):
         raise ValueError("rq_rotary: freq [rot_dim / 2], out of x's shape, positions int64 [B, n_tok] expected")
     H2, p2 = 0, (None, None, None, None)
@@ -372,7 +372,7 @@ def rq_rotary(x, out, positions, freq, rot_dim, style, scale=1.0, inverse=False,
         raise TypeError("rq_rotary: out has another dtype than x")
     _call("rq_rotary", x, stream, (
         x.data_ptr(), _strides(x, "x"), out.data_ptr(), _strides(out, "out"), H, *p2, H2, _dtype_code(x), B, n, d,
-        rot_dim, style, positions.data_ptr(), ps[0], f.ctypes.data, scale, 1 if inverse else 0))
+        rot_dim, style, positions.data_ptr(), ps[0], f, scale, 1 if inverse else 0))
 
 
 def rq_evict_accumulate_workspace_bytes(G, n_q, T) -> int:
@@ -437,6 +437,6 @@ def qjl_tree_attention(q, k_new, v_new, tree_mask, m, proj, signs, sk_norms, T, 
         q.data_ptr(), _strides(q, "q"), k_new.data_ptr(), _strides(k_new, "k_new"), v_new.data_ptr(),
         _strides(v_new, "v_new"), B, kv, H // kv, n, d, _ptr(tree_mask), stride, m, proj.data_ptr(), _dtype_code(proj),
         _ptr(signs), _ptr(sk_norms), T, _ptr(kv_len), _ptr(codes), _ptr(norms), bits, layout, int(use_signs),
-        sign_seed, None if c is None else c.ctypes.data, _ptr(v_codes), _ptr(v_norms), v_bits, v_layout,
-        int(v_use_signs), v_sign_seed, vc.ctypes.data, softmax_scale, out.data_ptr(), _strides(out, "out"),
+        sign_seed, c, _ptr(v_codes), _ptr(v_norms), v_bits, v_layout,
+        int(v_use_signs), v_sign_seed, vc, softmax_scale, out.data_ptr(), _strides(out, "out"),
         workspace.data_ptr(), workspace.numel() * workspace.element_size()))
