@@ -385,22 +385,17 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t quarter = (uint32_t)(warp & 3);
     tr_launch_next();
+    // lookup tables: one entry a thread, its copies by 16-byte stores whose order differs from lane to lane
     auto fill = [&](const QuantTables &T, uint8_t *dst, int pw, int cl) {
         if (pw == 0) return;
-        if (pw <= 4) {
-            uint32_t *lut = reinterpret_cast<uint32_t *>(dst);
-            for (int i = tid; i < 1 << (2 * pw + cl); i += threads) {
-                const int e = i >> cl, ca = e & ((1 << pw) - 1), cb = e >> pw;
-                const float fa = ca < T.levels ? T.centroid[ca] : 0.0f, fb = cb < T.levels ? T.centroid[cb] : 0.0f;
-                lut[i] = (uint32_t)__half_as_ushort(__float2half_rn(fa)) |
-                         ((uint32_t)__half_as_ushort(__float2half_rn(fb)) << 16);
-            }
-        } else {
-            uint16_t *l16 = reinterpret_cast<uint16_t *>(dst);
-            for (int i = tid; i < 256 << cl; i += threads) {
-                const int e = i >> cl;
-                l16[i] = __half_as_ushort(__float2half_rn(e < T.levels ? T.centroid[e] : 0.0f));
-            }
+        const int entries = pw <= 4 ? 1 << (2 * pw) : 256, bytes = (pw <= 4 ? 4 : 2) << cl, chunks = bytes / 16;
+        for (int e = tid; e < entries; e += threads) {
+            const int ca = pw <= 4 ? e & ((1 << pw) - 1) : e, cb = pw <= 4 ? e >> pw : e;
+            const float fa = ca < T.levels ? T.centroid[ca] : 0.0f, fb = cb < T.levels ? T.centroid[cb] : 0.0f;
+            const uint32_t v = (uint32_t)__half_as_ushort(__float2half_rn(fa)) |
+                               ((uint32_t)__half_as_ushort(__float2half_rn(fb)) << 16);
+            for (int i = 0; i < chunks; ++i)
+                tr_sts128(smem_u32(dst) + (uint32_t)(e * bytes) + (uint32_t)(((i + tid) & (chunks - 1)) * 16), v, v, v, v);
         }
     };
     if (TWO) fill(TK, klut, a.pw, KCL);
