@@ -356,3 +356,27 @@ def test_wide_trees(n, rep, T):
     got = run(c, q, kn, vn, mask, m, max(T, 1), lens, 0, 4, 0.09)
     kt, vt = vectors(c, 1, max(T, 1), m, 0, 4)
     check(got, kt, vt, q, kn, vn, mask, lens, 0.09)
+
+
+@pytest.mark.parametrize("n", [4, 40, 80])
+def test_hard_maximum(n):
+    """Queries equal to cached keys and a scale so large that one key carries all the weight: its value (the weights are
+    exact, so 2^-9 of the largest value and the output's rounding remain); later tiles move every reference far."""
+    T, m = 900, 256
+    k = torch.randn(1, T, D, device=DEV, generator=torch.Generator(device=DEV).manual_seed(95)).bfloat16()
+    picks = torch.linspace(0, T - 1, n, device=DEV).long()
+    c = compress(1, T, D, m, 0, 4, 95, False, k=k.reshape(-1))
+    q = k[0, picks].reshape(1, n, 1, D).contiguous()
+    kn = torch.zeros(1, n, 1, D, device=DEV, dtype=torch.bfloat16)
+    kt, vt = vectors(c, 1, T, m, 0, 4)
+    logits = q[0, :, 0].double() @ kt[0].T
+    top = logits.topk(2, -1)
+    sure = (top.values[:, 0] - top.values[:, 1]) > 0.05 * top.values[:, 0]
+    assert torch.equal(top.indices[sure, 0], picks[sure]) and int(sure.sum()) > n // 2
+    gap = float((top.values[sure, 0] - top.values[sure, 1]).min())
+    scale = 300.0 / gap                                        # 2^-400 on every other key; logits in the thousands
+    got = run(c, q, kn, kn, torch.zeros(1, n, (n + 63) // 64, dtype=torch.int64, device=DEV), m, T, None, 0, 4, scale)
+    want = vt[0, picks]
+    tol = 2.0 ** -9 * vt.norm(dim=-1).amax() + 2.0 ** -8 * want.abs()
+    assert torch.isfinite(got).all()
+    assert ((got[0, :, 0].double() - want).abs() <= tol)[sure].all()
