@@ -412,7 +412,8 @@ size_t rq_evict_accumulate_workspace_bytes(int64_t G, int n_q, int64_t T);
  *   scores fp32 [G][n_q][T] (qjl_score); row_len: int32 [G][n_q], query (g, q)
  *   sees tokens t < row_len (clamped to 0 .. T), or NULL: all T.  A query that
  *   sees nothing, or only scores of -inf, adds nothing; what lies behind its
- *   length is not read as a score (NaN there does no harm).
+ *   length is not read as a score (NaN there does no harm).  softmax_scale >= 0;
+ *   at 0 all scores but -inf weigh the same.
  *   acc fp32 [G][T] (not read, and may be NULL, when decay = 0); out fp32
  *   [G][T], may be acc.  The sum runs in query order: no atomics, so the same
  *   call gives the same bits. */

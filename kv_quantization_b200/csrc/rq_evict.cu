@@ -26,6 +26,14 @@ __device__ __forceinline__ float ac_exp2(float x)
     return y;
 }
 
+// Exponents are (s - m) k in units of log2.  k is never 0, so that a score of -inf, and the maximum of a part without
+// any score, keep their weight of 0 at every scale (-inf * 0 would be NaN): at scale 0 the smallest number, which
+// leaves the exponent of any finite score at 0 to within 2^-20.
+__device__ __forceinline__ float ac_factor(const AccumulateArgs &a)
+{
+    return fmaxf(a.scale * 1.4426950408889634074f, 0x1p-149f);
+}
+
 __device__ __forceinline__ int64_t ac_row_len(const AccumulateArgs &a, int64_t row)
 {
     if (!a.row_len) return a.T;
@@ -42,7 +50,7 @@ accumulate_stats_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks)
     const int64_t g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * kAcChunk;
-    const float k = a.scale * 1.4426950408889634074f;
+    const float k = ac_factor(a);
     for (int r = warp; r < a.nq; r += kAcThreads / 32) {
         const int64_t row = g * a.nq + r;
         const int64_t left = ac_row_len(a, row) - t0;
@@ -89,7 +97,7 @@ accumulate_columns_kernel(const __grid_constant__ AccumulateArgs a, int n_chunks
     const int64_t g = gridDim.y - 1 - blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * kAcChunk;
-    const float k = a.scale * 1.4426950408889634074f;
+    const float k = ac_factor(a);
     for (int r = warp; r < a.nq; r += kAcThreads / 32) {
         const float2 *p = reinterpret_cast<const float2 *>(a.workspace) + (g * a.nq + r) * n_chunks;
         float m = -INFINITY, l = 0.0f;

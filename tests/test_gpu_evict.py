@@ -100,6 +100,36 @@ def test_accumulate_special_scores():
     assert ((got - want).abs() <= 2.0 ** -16 * want).all()      # sums of 1500 ones in fp32 chains of under 64
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-45])
+@pytest.mark.parametrize("T", [3, 1500, 4096, 9001])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_accumulate_with_a_zero_scale(scale, T, ragged):
+    """Every score that a query sees weighs the same, but for -inf, which has no weight at any scale.  The weights are
+    1 / n, n a whole number: the reciprocal and the sum over 5 queries round, 2^-24 each, and 1e-45 of a score of at
+    most 100 moves no weight."""
+    G, R = 3, 5
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    scores = (torch.randn(G, R, T, generator=g, device=DEV) * 11).clamp(-100, 100)
+    scores[:, 1, ::3] = -math.inf
+    scores[:, 2] = -math.inf                                    # adds nothing
+    seen = torch.ones(G, R, T, dtype=torch.bool, device=DEV)
+    row_len = None
+    if ragged:
+        row_len = torch.randint(1, T + 1, (G, R), generator=g, device=DEV, dtype=torch.int32)
+        row_len[0, 0], row_len[1, 4] = 0, T
+        seen = torch.arange(T, device=DEV) < row_len[..., None]
+        scores = torch.where(seen, scores, math.nan)
+    live = (seen & (scores != -math.inf)).double()
+    want = (live / live.sum(-1, keepdim=True).clamp_min(1.0)).sum(1)
+    acc = torch.rand(G, T, generator=g, device=DEV)
+    got = accumulate(scores, scale, 0.0, None, row_len)
+    assert ((got.double() - want).abs() <= 8 * 2.0 ** -24 * want).all()
+    io = acc.clone()                                            # in place: the old sums are not lost
+    accumulate(scores, scale, 1.0, io, row_len, out=io)
+    assert ((io.double() - acc.double() - want).abs() <= 2.0 ** -24 * (acc + want) + 8 * 2.0 ** -24 * want).all()
+
+
 def test_accumulate_far_offsets():
     """Scores past 2^31 elements and 2^32 bytes."""
     G, R, T = 9, 8, 1 << 25
