@@ -7,7 +7,7 @@
 // With one node it is the ordinary decode step.
 //
 // Three kernels:
-//   tree_prologue_kernel   the score operand of every row, [H D q ; S q] / |q| in fp16, written as the image of the
+//   tree_prologue_kernel   the score operand of every row, [H D q ; S q] 2^-e in fp16, written as the image of the
 //                          shared-memory operand (so that the main kernel fetches it with one bulk copy); the
 //                          prefix sums of the groups' tiles;
 //   tree_attention_kernel  the cached part, split evenly over the SMs whatever the lengths: (m, l, O) per segment;
@@ -43,6 +43,12 @@ constexpr int kTrD = 128;
 constexpr int kTrVBytes = kTrTok * kTrD * 2;      // one value tile, fp16
 constexpr float kTrShift = 8.0f;                  // weight of the reference: 2^8
 constexpr float kTrMost = 15.0f;                  // largest exponent an fp16 weight may have
+// The score operand of a row in fp16 is [H D q ; S q] 2^-e / 16, 2^e <= max |q_i| < 2^(e + 1): at most |S_i| sqrt(2), and
+// for a pure sketch times 2 .. 2^-7 (tr_bit_factor).  Rows of a chunk of 32 whose e are within kTrSpread share the
+// largest: the smallest of them still lies 2^-13 high where S is N(0, 1) and a half step of fp16 is 2^-25, as precise as
+// a normal fp16 value.  In a chunk with a wider spread every row has its own e, and the softmax multiplies by it.
+constexpr int kTrSpread = 4;
+constexpr float kTrRowScale = 16.0f;
 
 constexpr int kTrAhead = 4;                       // tiles that the cache's records are prefetched into L2 ahead
 
@@ -67,10 +73,13 @@ __host__ __device__ inline size_t tr_lut_bytes(int pw, int cl)
 {
     return pw == 0 ? 0 : pw <= 4 ? ((size_t)4 << (2 * pw + cl)) : ((size_t)512 << cl);
 }
+// mbarriers: key slots full and empty, values, scores full and empty, weights (2 each), P V done (4), O, the operand full
+// and done, and a vote by group of softmax warps
+__host__ __device__ constexpr int tr_barriers(int nb) { return 2 * tr_kslots(nb) + 4 * 2 + 4 + 3 + tr_softmax_warps(nb) / 4; }
 __host__ __device__ inline size_t tr_smem(int nb, int kb, int pw, int vpw, int np, int nv)
 {
     return 1024 + (size_t)nb * kb * 2 + nv * kTrVBytes + np * tr_pbytes(nb) + tr_lut_bytes(pw, tr_kcl(nb)) +
-           tr_lut_bytes(vpw, tr_vcl(nb)) + 2048 + (size_t)nb * 12 + (size_t)5 * nb * 4 + 8 * 40 + 48;
+           tr_lut_bytes(vpw, tr_vcl(nb)) + 2048 + (size_t)nb * (8 + 4 + 4 + 5 * 4) + 8 * tr_barriers(nb) + 4 + tr_softmax_warps(nb) * 2;
 }
 // Partial result of one (CTA, row block) segment: O [nb][128], m [nb], l [nb].
 __host__ __device__ inline size_t tr_part_floats(int nb) { return (size_t)nb * (kTrD + 2); }
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(tr_threads(NB), tr_ctas(NB))
 tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ QuantTables TK,
                       const __grid_constant__ QuantTables TV, int np, int nv)
 {
-    constexpr int SW = tr_softmax_warps(NB), NPG = tr_producer_groups(NB), PW = 4 * NPG;
+    constexpr int SW = tr_softmax_warps(NB), NG = SW / 4, NPG = tr_producer_groups(NB), PW = 4 * NPG;
     constexpr int VCL = tr_vcl(NB), KCL = tr_kcl(NB), threads = tr_threads(NB), KS = tr_kslots(NB), NS = tr_sbufs(NB);
     // Every producer group has its own key slots: it may be tiles ahead of the products, but then never more than one
     // phase ahead of a slot's barrier, which is what a parity can tell.
@@ -368,7 +377,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     float4 *sF = reinterpret_cast<float4 *>(vlut + tr_lut_bytes(a.vpw, VCL));
     float *sAl = reinterpret_cast<float *>(sF + NB / 2);                         // [NB] rescale factors
     float *sX = sAl + NB;                         // [4][NB] column reductions by lane quarter, [NB] moves of the exponents
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(sX + 5 * NB);
+    float *sR = sX + 5 * NB;                      // [NB] factors of the rows, for chunks in which they differ
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(sR + NB);
     uint64_t *k_empty = k_full + KS;
     uint64_t *v_full = k_empty + KS;              // [2]
     uint64_t *s_full = v_full + 2;                // [2]
@@ -378,9 +388,9 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     uint64_t *o_empty = pv_done + 4;
     uint64_t *q_full = o_empty + 1;
     uint64_t *q_done = q_full + 1;
-    uint64_t *vote = q_done + 1;                  // [4] by softmax group
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(vote + 4);
-    volatile uint32_t *flag = tmem_slot + 1;      // [4][2] by softmax group and use parity
+    uint64_t *vote = q_done + 1;                  // by softmax group
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(vote + NG);
+    volatile uint32_t *flag = tmem_slot + 1;      // [NG][2] by softmax group and use parity
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t quarter = (uint32_t)(warp & 3);
@@ -403,8 +413,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     for (int i = tid; i < 512; i += threads) reinterpret_cast<uint32_t *>(ones)[i] = 0x3C003C00u;
     fence_proxy_async_smem();
     if (tid == 0) {
-        for (int b = 0; b < 8; ++b) flag[b] = 0u;
-        for (int b = 0; b < 4; ++b) mbar_init(&vote[b], 4);
+        for (int b = 0; b < 2 * NG; ++b) flag[b] = 0u;
+        for (int b = 0; b < NG; ++b) mbar_init(&vote[b], 4);
         for (int b = 0; b < KS; ++b) { mbar_init(&k_full[b], 4); mbar_init(&k_empty[b], 1); }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&v_full[b], 4);
@@ -674,33 +684,37 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         // ------------------------------------------------------------ softmax
         const int wg = warp >> 2, cb = wg * 32, wt = tid & 127, bar = 1 + wg;     // rows cb .. cb + 31
         const int r = (int)quarter * 32 + lane;                 // token of the tile
-        const uint32_t lanes = quarter << 21, sP0 = smem_u32(sP), sF0 = smem_u32(sF) + (uint32_t)cb * 8u;
+        const uint32_t lanes = quarter << 21, sP0 = smem_u32(sP), sF0 = smem_u32(sF) + (uint32_t)cb * 8u, sR0 = smem_u32(sR + cb);
         const uint16_t *gsrc = TWO ? a.norms : a.sk_norms;
-        const float gk = TWO ? 1.0f / (float)kTrD : 1.2533141373155002512f / (float)a.m * kTrBitScale;
+        const float gk = kTrRowScale * (TWO ? 1.0f / (float)kTrD : 1.2533141373155002512f / (float)a.m * kTrBitScale);
         uint16_t gn = r < it.left ? __ldg(gsrc + it.row + r) : (uint16_t)0;
-        float ref = -INFINITY, cq = 0.0f;                       // reference of row cb + wt (wt < 32); the chunk's factor
+        float ref = -INFINITY;                                  // reference of row cb + wt (wt < 32)
+        float cq = 0.0f;                                        // the chunk's factor; -1: its rows have their own
         bool fresh = true;
         uint32_t use = 0;                                       // votes so far
         for (int c = 0; c < count; ++c) {                       // every item and barrier also after a wait has expired
             const bool start = fresh;
             if (start) {
+                const float fr = a.wsC[(it.g * a.rbs + it.rb) * NB + cb + lane];
+                cq = __shfl_sync(0xffffffffu, fr, 0);
+                if (!__all_sync(0xffffffffu, fr == cq)) cq = -1.0f;
                 if (wt < 32) {
                     const int row = cb + wt;
+                    sR[row] = fr;
                     float sum = 0.0f;
                     if (!TWO) {
                         const float *wc = a.wsC + ((int64_t)a.G * a.rbs + it.g * a.rbs + it.rb) * NB + row;
                         for (int i = 0; i < 2 * nsl; ++i) sum += wc[(int64_t)i * a.G * a.rbs * NB];
                     }
                     float *f = reinterpret_cast<float *>(sF + (row >> 1)) + (row & 1);
-                    f[0] = sum * (-1.0f / kTrBitScale);
+                    f[0] = sum * (-1.0f / kTrBitScale) * (cq < 0.0f ? fr : 1.0f);
                     f[2] = 0.0f;
                 }
                 ref = -INFINITY;
-                cq = a.wsC[(it.g * a.rbs + it.rb) * NB + cb];
                 tr_bar(bar);
             }
             const bool valid = r < it.left;
-            const float gg = __fmul_rn(__fmul_rn(h16_to_f32(gn), gk), cq);
+            const float gg = __fmul_rn(__fmul_rn(h16_to_f32(gn), gk), fabsf(cq));
             const uint32_t vm = valid ? 0xffffffffu : 0u;
             const int64_t pg = it.g * a.rbs + it.rb;
             fresh = false;
@@ -717,6 +731,16 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             auto exponents = [&]() {
                 tmem_ld32(tS + (uint32_t)(c % NS * NB + cb) + lanes, sr);
                 tmem_ld_wait();
+                if (cq < 0.0f) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 x = tr_lds_f4(sR0 + (uint32_t)j * 4u);
+                        const float2 lo = __fmul2_rn(make_float2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), make_float2(x.x, x.y));
+                        const float2 hi = __fmul2_rn(make_float2(__uint_as_float(sr[j + 2]), __uint_as_float(sr[j + 3])), make_float2(x.z, x.w));
+                        sr[j] = __float_as_uint(lo.x); sr[j + 1] = __float_as_uint(lo.y);
+                        sr[j + 2] = __float_as_uint(hi.x); sr[j + 3] = __float_as_uint(hi.y);
+                    }
+                }
                 float mx = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
@@ -850,7 +874,7 @@ __device__ __forceinline__ const uint16_t *tr_row(const uint16_t *p, const rq_st
 }
 
 // Grid (32-row tiles of every row block, 64-column slices); 4 warps, each 16 rows x 32 columns of
-//   [q H D ; q S^T] / max |q| of the 32 rows
+//   [q H D ; q S^T] 2^-e / 16
 // as bf16 products with fp32 sums: the entries of H D are +-1, an fp16 projection is the sum of two bf16 numbers, so
 // every product is exact.  A thread's 128-value rows are loaded as 64 contiguous bytes a lane of the quad; the sum
 // over k runs in that order for both operands.  CTA (0, 0) also writes the prefix sums of the groups' tiles.
@@ -894,38 +918,50 @@ tree_prologue_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__
     const int s = blockIdx.y, dsl = a.pw ? 2 : 0;
     // rows row0 + rr and + 8 of the block, elements 32 p .. 32 p + 31
     uint32_t A[2][16];
-    float ss[2];
+    uint32_t top[2];                                            // bits of the row's largest |element|
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int r = rb * a.nb + row0 + rr + 8 * h;
         const bool in = r < a.rows;
         const uint4 *src = in ? reinterpret_cast<const uint4 *>(tr_row(a.q, a.qs, a, g, r) + 32 * p) : nullptr;
-        ss[h] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint4 v = in ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
             A[h][4 * i] = v.x; A[h][4 * i + 1] = v.y; A[h][4 * i + 2] = v.z; A[h][4 * i + 3] = v.w;
         }
+        uint32_t mx = 0u;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float x = bf16_lo(A[h][i]), y = bf16_hi(A[h][i]);
-            ss[h] = __fmaf_rn(x, x, __fmaf_rn(y, y, ss[h]));
-        }
-        ss[h] += __shfl_xor_sync(0xffffffffu, ss[h], 1);
-        ss[h] += __shfl_xor_sync(0xffffffffu, ss[h], 2);
+        for (int i = 0; i < 16; ++i) mx = __vmaxu2(mx, A[h][i] & 0x7fff7fffu);
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        top[h] = max(mx & 0xffffu, mx >> 16);
     }
-    // one factor for the chunk's 32 rows, the largest finite |q| (a row whose own is not finite comes out NaN by itself)
-    __shared__ float norm[32];
-    const float n0 = sqrtf(ss[0]), n1 = sqrtf(ss[1]);
+    // exponents (biased by 127) of the chunk's rows; 0: a row of zeros, or one that is not finite, which comes out NaN by
+    // itself whatever its factor
+    __shared__ int exps[32];
     if (p == 0) {
-        norm[(warp & 1) * 16 + rr] = n0 < INFINITY ? n0 : 0.0f;
-        norm[(warp & 1) * 16 + rr + 8] = n1 < INFINITY ? n1 : 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            exps[(warp & 1) * 16 + rr + 8 * h] = top[h] == 0u || top[h] >= 0x7f80u ? 0 : min(max((int)(top[h] >> 7), 1), 253);
     }
     __syncthreads();
-    float nmax = norm[lane];
-    for (int o = 16; o > 0; o >>= 1) nmax = fmaxf(nmax, __shfl_xor_sync(0xffffffffu, nmax, o));
-    const float inv = nmax > 0.0f ? 1.0f / nmax : 0.0f;
-    if (s == 0 && tid == 0) a.wsC[pg * a.nb + row0] = nmax * a.qscale;
+    const int ex = exps[lane];
+    const int most = __reduce_max_sync(0xffffffffu, ex), least = __reduce_min_sync(0xffffffffu, ex > 0 ? ex : 255);
+    const bool wide = most - least > kTrSpread;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = (warp & 1) * 16 + rr + 8 * h;
+        const int own = wide ? exps[row] : most, e = own > 0 ? own : 127;
+        // exact, but for elements 2^-126 of the largest
+        const uint32_t down = (uint32_t)(254 - e) << 7, down2 = down | (down << 16);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&A[h][i]), *reinterpret_cast<const __nv_bfloat162 *>(&down2));
+            A[h][i] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        if (s == 0 && warp < 2 && p == 0)
+            a.wsC[pg * a.nb + row0 + rr + 8 * h] = __uint_as_float((uint32_t)e << 23) * a.qscale;
+    }
     uint32_t Bs[4][16];                                         // four operand rows, loaded at once
     if (s >= dsl) {
 #pragma unroll
@@ -986,7 +1022,7 @@ tree_prologue_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__
         for (int e = 0; e < 4; ++e) {
             const int r = row0 + rr + (e >> 1) * 8;
             int col = (warp >> 1) * 32 + n8 * 8 + 2 * p + (e & 1);
-            float x = d[e] * inv;
+            float x = d[e] * (1.0f / kTrRowScale);
             const float f = tr_bit_factor(col);
             if (!a.pw) x *= f;                                   // by a power of two
             const __half h = __float2half_rn(x);

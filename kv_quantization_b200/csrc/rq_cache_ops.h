@@ -89,7 +89,7 @@ struct TreeArgs {
     // set by tree_plan / launch_tree
     int nb, rbs, kb;                       // query rows a block, row blocks a group, score operand width
     uint8_t *wsQ;                          // operand images [G rbs][kb / 64][nb][128 B]
-    float *wsC;                            // [1 + kb / 32][G rbs][nb]: max |q| qscale of 32 rows at the first, then sums of 32 operand coordinates
+    float *wsC;                            // [1 + kb / 32][G rbs][nb]: 2^e qscale of the rows, then sums of 32 operand coordinates
     int64_t *off;                          // [G + 1] prefix sums of the groups' tiles
     float *part;
 };

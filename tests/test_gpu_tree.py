@@ -380,3 +380,55 @@ def test_hard_maximum(n):
     tol = 2.0 ** -9 * vt.norm(dim=-1).amax() + 2.0 ** -8 * want.abs()
     assert torch.isfinite(got).all()
     assert ((got[0, :, 0].double() - want).abs() <= tol)[sure].all()
+
+
+@pytest.mark.parametrize("factor", [1e-20, 1e4, 1e12, 1e20])
+@pytest.mark.parametrize("n,rep,m,kbits", [(4, 4, 256, 0), (20, 2, 128, 2), (40, 2, 256, 0), (40, 2, 128, 3)])
+def test_rows_of_very_different_norms(n, rep, m, kbits, factor):
+    """One query row that is far longer (a drafted place that holds rubbish), or far shorter, than its neighbours: their
+    outputs stay within the bar, and the long row finds its key."""
+    T, at, key = 900, (0, 2, 1), 77
+    k = torch.randn(1, T, D, device=DEV, generator=torch.Generator(device=DEV).manual_seed(97)).bfloat16()
+    c = compress(1, T, D, m, kbits, 4, 97, kbits > 0, k=k.reshape(-1))
+    q, kn, vn = drafted(1, n, 1, rep, 98)
+    q[at] = k[0, key]
+    kn[:], mask = 0, torch.zeros(1, n, (n + 63) // 64, dtype=torch.int64, device=DEV)
+    kt, vt = vectors(c, 1, T, m, kbits, 4)
+    scale = 1 / math.sqrt(D)
+    odd = q.clone()
+    odd[at] = (q[at].float() * factor).bfloat16()
+    got = run(c, odd, kn, vn, mask, m, T, None, kbits, 4, scale)
+    torch.cuda.synchronize()
+    assert L.rq_device_error(True) == 0
+    assert torch.isfinite(got).all()
+    if factor < 1:
+        check(got, kt, vt, odd, kn, vn, mask, None, scale)
+        return
+    # the next key is 5 % behind at least: with the logits this large all weight is on `key`, exactly
+    logits = (odd[at].double() @ kt[0].T) * scale
+    top = logits.topk(2)
+    assert int(top.indices[0]) == key and float(top.values[0] - top.values[1]) > max(0.05 * float(top.values[0]), 200.0)
+    tol = 2.0 ** -9 * vt.norm(dim=-1).amax() + 2.0 ** -8 * vt[0, key].abs()
+    assert ((got[at].double() - vt[0, key]).abs() <= tol).all()
+    plain = run(c, q, kn, vn, mask, m, T, None, kbits, 4, scale)
+    got[at] = plain[at]
+    check(got, kt, vt, q, kn, vn, mask, None, scale)
+
+
+def test_long_zero_and_nan_rows_side_by_side():
+    """One chunk of rows that holds a row of 1e20, a zero one, a NaN one and one of 1e-30 times the others."""
+    T, m, n, rep = 700, 256, 6, 4
+    c = compress(1, T, D, m, 0, 4, 99, False)
+    q, kn, vn = drafted(1, n, 1, rep, 99)
+    plain = run(c, q, kn, vn, None, m, T, None, 0, 4, 0.1)
+    odd = q.clone()
+    odd[0, 1, 2] = 0.0
+    odd[0, 4, 0] = (q[0, 4, 0].float() * 1e-30).bfloat16()
+    quiet = odd.clone()
+    odd[0, 2, 1] = (q[0, 2, 1].float() * 1e20).bfloat16()
+    odd[0, 3, 3, 7] = math.nan
+    got = run(c, odd, kn, vn, None, m, T, None, 0, 4, 0.1)
+    assert torch.isfinite(got[0, 2, 1]).all() and torch.isnan(got[0, 3, 3]).all()
+    got[0, 2, 1], got[0, 3, 3] = plain[0, 2, 1], plain[0, 3, 3]
+    kt, vt = vectors(c, 1, T, m, 0, 4)
+    check(got, kt, vt, quiet, kn, vn, None, None, 0.1)
