@@ -1,6 +1,8 @@
 // qjl_tree.cu -- launcher of the attention of drafted tokens over the compressed cache (kernels in qjl_tree.cuh).
 #include "qjl_tree.cuh"
 
+#include <cmath>
+
 namespace rq {
 
 namespace {
@@ -107,6 +109,14 @@ cudaError_t launch_tree(const TreeArgs &in, const QuantTables &tk, const QuantTa
     a.wsC = reinterpret_cast<float *>(ws + p.c);
     a.off = reinterpret_cast<int64_t *>(ws + p.off);
     a.part = reinterpret_cast<float *>(ws + p.part);
+    // value centroids as c 2^-e, below 1: times a norm of at most 65504 they fit fp16
+    float top = 0.0f;
+    for (int i = 0; i < tv.levels; ++i) top = std::fmax(top, std::fabs(tv.centroid[i]));
+    int e = 0;
+    std::frexp(top, &e);
+    e = e < -100 ? -100 : e;
+    a.vdown = std::ldexp(1.0f, -e);
+    a.vup = std::ldexp(1.0f / (float)kTrD, e);
     const int grid = (int)tree_grid(a.G, a.rbs, a.nb, a.T, a.num_sms);
     if (grid > 0) {
         tree_prologue_kernel<<<dim3((unsigned)(a.G * a.rbs * (a.nb / 32)), (unsigned)(a.kb / 64)), 128, 0, st>>>(a, tk);

@@ -18,7 +18,8 @@
 // token-wise factors are its own registers:
 //   producers (groups of 4 warps)  thread = token: 64 key values a slice are unpacked to fp16 and stored to TMEM, where
 //                        the score product reads its A operand: unpacked keys never pass through shared memory.  Then
-//                        the token's values, V' = fp16(c) * fp16(n / d), to shared memory.
+//                        the token's values, V' = fp16(c 2^-e) n, to shared memory (2^e above the largest centroid, so
+//                        that V' fits fp16 whatever the norm; the rest of the factor, 2^e / d, is the join's).
 //   MMA 1 (one thread)   S^T[token][row] += K slice (TMEM) . Q^T slice (shared memory).
 //   softmax (4 warps for 32 rows)  thread = token: weights 2^((s - Q) g + 8 - ref), fp16, to shared memory.  The reference
 //                        `ref` of a row is the maximum of the segment's first tile and moves only when a score passes
@@ -396,20 +397,20 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     const uint32_t quarter = (uint32_t)(warp & 3);
     tr_launch_next();
     // lookup tables: one entry a thread, its copies by 16-byte stores whose order differs from lane to lane
-    auto fill = [&](const QuantTables &T, uint8_t *dst, int pw, int cl) {
+    auto fill = [&](const QuantTables &T, uint8_t *dst, int pw, int cl, float by) {
         if (pw == 0) return;
         const int entries = pw <= 4 ? 1 << (2 * pw) : 256, bytes = (pw <= 4 ? 4 : 2) << cl, chunks = bytes / 16;
         for (int e = tid; e < entries; e += threads) {
             const int ca = pw <= 4 ? e & ((1 << pw) - 1) : e, cb = pw <= 4 ? e >> pw : e;
-            const float fa = ca < T.levels ? T.centroid[ca] : 0.0f, fb = cb < T.levels ? T.centroid[cb] : 0.0f;
+            const float fa = ca < T.levels ? T.centroid[ca] * by : 0.0f, fb = cb < T.levels ? T.centroid[cb] * by : 0.0f;
             const uint32_t v = (uint32_t)__half_as_ushort(__float2half_rn(fa)) |
                                ((uint32_t)__half_as_ushort(__float2half_rn(fb)) << 16);
             for (int i = 0; i < chunks; ++i)
                 tr_sts128(smem_u32(dst) + (uint32_t)(e * bytes) + (uint32_t)(((i + tid) & (chunks - 1)) * 16), v, v, v, v);
         }
     };
-    if (TWO) fill(TK, klut, a.pw, KCL);
-    fill(TV, vlut, a.vpw, VCL);
+    if (TWO) fill(TK, klut, a.pw, KCL, 1.0f);
+    fill(TV, vlut, a.vpw, VCL, a.vdown);
     for (int i = tid; i < 512; i += threads) reinterpret_cast<uint32_t *>(ones)[i] = 0x3C003C00u;
     fence_proxy_async_smem();
     if (tid == 0) {
@@ -553,8 +554,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                 load_norms(it);
             }
             // the value row: rows of tokens, two 64-wide atoms of d
-            const float fv = __fmul_rn(h16_to_f32(hv), 1.0f / (float)kTrD);
-            const __half2 f2 = __half2half2(__float2half_rn(fv));
+            const __half2 f2 = __half2half2(__ushort_as_half(hv));
             const int vb = nv == 2 ? c & 1 : 0;
             uint32_t Vr = sV0 + (uint32_t)vb * kTrVBytes + (uint32_t)r * 128u;
 #pragma unroll 1
@@ -1216,7 +1216,7 @@ tree_combine_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ 
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + h0 + i;
         if (r >= a.rows) break;
-        const float x = (neg ? -acc[i] : acc[i]) + ot[i], l = sL[h0 + i];
+        const float x = __fmaf_rn(neg ? -acc[i] : acc[i], a.vup, ot[i]), l = sL[h0 + i];
         const float y = l == 0.0f ? 0.0f : __fdiv_rn(x, l);
         uint16_t *dst = const_cast<uint16_t *>(tr_row(a.out, a.os, a, g, r));
         dst[d] = (uint16_t)(pack2<true>(y, 0.0f) & 0xffffu);

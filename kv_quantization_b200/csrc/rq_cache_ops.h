@@ -92,6 +92,7 @@ struct TreeArgs {
     float *wsC;                            // [1 + kb / 32][G rbs][nb]: 2^e qscale of the rows, then sums of 32 operand coordinates
     int64_t *off;                          // [G + 1] prefix sums of the groups' tiles
     float *part;
+    float vdown, vup;                      // 2^-e of the value centroids, and 2^e / d
 };
 constexpr int kTreeMaxNodes = 1024;
 bool tree_supported(int d, int m, int pw, int vpw);

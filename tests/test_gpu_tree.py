@@ -432,3 +432,22 @@ def test_long_zero_and_nan_rows_side_by_side():
     got[0, 2, 1], got[0, 3, 3] = plain[0, 2, 1], plain[0, 3, 3]
     kt, vt = vectors(c, 1, T, m, 0, 4)
     check(got, kt, vt, quiet, kn, vn, None, None, 0.1)
+
+
+@pytest.mark.parametrize("size,table", [(1e-4, 1.0), (1e-5, 1.0), (200.0, 2000.0), (1.0, 1e-6), (1.0, 1e3)])
+@pytest.mark.parametrize("n,rep,vbits", [(4, 4, 4), (40, 2, 4), (13, 3, 3), (13, 3, 8)])
+def test_values_of_every_size(n, rep, vbits, size, table):
+    """Value norms (11 size) from 1e-4 to thousands, and tables of any scale.  A cached value's coordinate c 2^-e n, with
+    2^e just above the largest centroid, is rounded to fp16: half a step is 2^-11 of it, or 2^-25 below 2^-14.  The
+    centroids' mean square is 1 and 2^e at most 8, so at n = 1.1e-4 the latter is 2^-25 8 / 1.1e-4 / sqrt(3) = 1.3e-3 of
+    the row, uncorrelated: within the 2e-3."""
+    T, m = 800, 128
+    v = (torch.randn(T, D, device=DEV, generator=torch.Generator(device=DEV).manual_seed(101)) * size).bfloat16()
+    c = compress(1, T, D, m, 0, vbits, 101, False, v=v.reshape(-1),
+                 vlayout=L.RQ_CODES_INT8 if vbits == 8 else L.RQ_CODES_PACKED)
+    c["vc"] = (c["vc"] * np.float32(table)).astype(np.float32)
+    q, kn, vn = drafted(1, n, 1, rep, 102)
+    vn = (vn.float() * (size * table)).bfloat16()
+    got = run(c, q, kn, vn, None, m, T, None, 0, vbits, 0.3)
+    kt, vt = vectors(c, 1, T, m, 0, vbits)
+    check(got, kt, vt, q, kn, vn, None, None, 0.3)
