@@ -75,8 +75,8 @@ __host__ __device__ inline size_t tr_lut_bytes(int pw, int cl)
     return pw == 0 ? 0 : pw <= 4 ? ((size_t)4 << (2 * pw + cl)) : ((size_t)512 << cl);
 }
 // mbarriers: key slots full and empty, values, scores full and empty, weights (2 each), P V done (4), O, the operand full
-// and done, and a vote by group of softmax warps
-__host__ __device__ constexpr int tr_barriers(int nb) { return 2 * tr_kslots(nb) + 4 * 2 + 4 + 3 + tr_softmax_warps(nb) / 4; }
+// and done, the last products of the two issuing warps, and a vote by group of softmax warps
+__host__ __device__ constexpr int tr_barriers(int nb) { return 2 * tr_kslots(nb) + 4 * 2 + 4 + 3 + 2 + tr_softmax_warps(nb) / 4; }
 __host__ __device__ inline size_t tr_smem(int nb, int kb, int pw, int vpw, int np, int nv)
 {
     return 1024 + (size_t)nb * kb * 2 + nv * kTrVBytes + np * tr_pbytes(nb) + tr_lut_bytes(pw, tr_kcl(nb)) +
@@ -133,6 +133,17 @@ __device__ __forceinline__ void tr_sts128(uint32_t addr, uint32_t x, uint32_t y,
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+// Waits between the roles have a limit, and none of them decides what a warp does next: after an expired wait (recorded
+// in the device error word) a warp goes through its remaining items like any other, with one poll for each wait.  So the
+// lanes of a warp never part, as elect.sync and the instructions for tensor memory need, and every warp comes to the same
+// barriers equally often.
+__device__ __forceinline__ void tr_wait(uint64_t *bar, uint32_t parity, uint32_t &limit)
+{
+    if (!mbar_wait_limit(bar, parity, limit)) limit = 1;
+}
+
+// A barrier of the four warps of a softmax group.  They take the same way (tr_vote_wait), and no other wait is without
+// limit, so all of them come to it.
 __device__ __forceinline__ void tr_bar(int id)
 {
     asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
@@ -141,6 +152,14 @@ __device__ __forceinline__ void tr_bar(int id)
 __device__ __forceinline__ void tr_arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The wait for the other warps of the group to have voted.  It is never cut short, so that all of them see the same votes:
+// between two places where the group meets (a vote, a barrier) a warp has at most four waits, each with the usual limit,
+// so this one ends before its own limit of 16 times that.
+__device__ __forceinline__ void tr_vote_wait(uint64_t *bar, uint32_t parity)
+{
+    mbar_wait_limit(bar, parity, 16 * kSpinLimit);
 }
 
 // True in one lane of a converged warp.  (Measured: products issued under `lane == 0` cost the issuing thread about 200
@@ -389,7 +408,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     uint64_t *o_empty = pv_done + 4;
     uint64_t *q_full = o_empty + 1;
     uint64_t *q_done = q_full + 1;
-    uint64_t *vote = q_done + 1;                  // by softmax group
+    uint64_t *drained = q_done + 1;               // [2] by issuing warp: all its products are done
+    uint64_t *vote = drained + 2;                 // by softmax group
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(vote + NG);
     volatile uint32_t *flag = tmem_slot + 1;      // [NG][2] by softmax group and use parity
 
@@ -426,6 +446,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         mbar_init(o_empty, SW);
         mbar_init(q_full, 1);
         mbar_init(q_done, 1);
+        for (int b = 0; b < 2; ++b) mbar_init(&drained[b], 1);
         fence_barrier_init();
     }
     if (warp == SW + PW) tmem_alloc(tmem_slot, tr_tmem(NB));
@@ -440,8 +461,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
     const int64_t total = a.off[a.G] * a.rbs, ctas = total < gridDim.x ? total : gridDim.x;
     const int64_t it0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
     const int count = blockIdx.x < ctas ? (int)(total * (blockIdx.x + 1) / ctas - it0) : 0;
-    bool ok = true;
-    auto pv_wait = [&](int tile) { return mbar_wait(&pv_done[tile & 3], (uint32_t)((tile >> 2) & 1)); };
+    uint32_t limit = kSpinLimit;
+    auto pv_wait = [&](int tile) { tr_wait(&pv_done[tile & 3], (uint32_t)((tile >> 2) & 1), limit); };
     TreeIter it;
     if (count > 0) it.seek(a, it0);
 
@@ -491,7 +512,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             load_signs(it, 0);
             load_norms(it);
         }
-        for (int c = group; c < count && ok; c += NPG) {
+        for (int c = group; c < count; c += NPG) {
             uint32_t rho2 = 0x3C003C00u;
             if (TWO) {
                 // the sketch term scaled to share the first stage's accumulator and factor n / d
@@ -525,7 +546,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                     sg[2] = sg[3];
                     if (s - dsl == 3 && nsig > 4) load_signs(it, 4);
                 }
-                if (n >= SPG && ok && !mbar_wait(&k_empty[slot], (n / SPG - 1) & 1)) ok = false;
+                if (n >= SPG) tr_wait(&k_empty[slot], (n / SPG - 1) & 1, limit);
                 tc_fence_after();
                 tmem_st32(tK + (uint32_t)slot * 32u + (quarter << 21), o);
                 tmem_st_wait();
@@ -560,7 +581,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
 #pragma unroll 1
             for (int half = 0; half < 2; ++half, Vr += kTrVBytes / 2) {
                 if (!V4 && a.vpw > 4) tr_load_codes<4, 8>(a.vcodes + row * vbytes + half * 8 * a.vpw, a.vpw, valid, vc);
-                if (half == 0 && c >= nv && ok && !pv_wait(c - nv)) ok = false;  // the tile whose values lie here.  With a
+                if (half == 0 && c >= nv) pv_wait(c - nv);      // the tile whose values lie here.  With a
                 // barrier for every fourth tile the phase before this one has been waited for (at this group's last
                 // tile) and the next one needs this tile's values, so the parity tells.
                 auto store = [&](int ch0, const uint32_t *o) {
@@ -594,27 +615,28 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         const uint32_t idesc = idesc_f16(false, kTrTok, NB);
         const uint32_t qbytes = (uint32_t)NB * kb * 2;
         bool fresh = true;
-        int seg = 0;
-        for (int c = 0; c < count && ok; ++c) {
+        int seg = 0, loads = 0;
+        for (int c = 0; c < count; ++c) {
             if (fresh) {
                 if (seg > 0) {
                     if (tr_elect()) mma_commit(q_done);
-                    if (!mbar_wait(q_done, (uint32_t)((seg - 1) & 1))) { ok = false; break; }
+                    tr_wait(q_done, (uint32_t)((seg - 1) & 1), limit);
                 }
-                if (lane == 0) {
+                loads += limit > 1;                             // (lane 0's)
+                if (lane == 0 && limit > 1) {
                     mbar_arrive_expect_tx(q_full, qbytes);
                     bulk_load(sQ, a.wsQ + (it.g * a.rbs + it.rb) * (int64_t)qbytes, qbytes, q_full);
                 }
-                if (!mbar_wait(q_full, (uint32_t)(seg & 1))) { ok = false; break; }
+                tr_wait(q_full, (uint32_t)(seg & 1), limit);
                 ++seg;
             }
             const int before = c - NS;                          // the tile whose scores lie in the buffer
-            if (before >= 0 && !mbar_wait(&s_empty[before & 1], (uint32_t)((before >> 1) & 1))) { ok = false; break; }
+            if (before >= 0) tr_wait(&s_empty[before & 1], (uint32_t)((before >> 1) & 1), limit);
             tc_fence_after();
             for (int s = 0; s < nsl; ++s) {
                 const uint32_t n = (uint32_t)(c / NPG * nsl + s);
                 const int slot = c % NPG * SPG + (int)(n % SPG);
-                if (!mbar_wait(&k_full[slot], (n / SPG) & 1)) { ok = false; break; }
+                tr_wait(&k_full[slot], (n / SPG) & 1, limit);
                 tc_fence_after();
                 if (tr_elect()) {
 #pragma unroll
@@ -629,10 +651,11 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             }
             if (c + 1 < count) fresh = it.next(a);
         }
-        if (seg > 0) {                                          // all products done before TMEM is freed
-            if (tr_elect()) mma_commit(q_done);
-            if (ok) mbar_wait(q_done, (uint32_t)((seg - 1) & 1));
-        }
+        // all copies and products done before shared memory and TMEM are freed, also after an expired wait
+        loads = __shfl_sync(0xffffffffu, loads, 0);
+        if (loads > 0) mbar_wait(q_full, (uint32_t)((loads - 1) & 1));
+        if (tr_elect()) mma_commit(&drained[0]);
+        mbar_wait(&drained[0], 0);
     } else if (count > 0 && warp == SW + PW + 1) {
         // ------------------------------------------------------------ MMA 2: O^T += V'^T . P; L2 prefetch
         const uint32_t sP0 = smem_u32(sP), sV0 = smem_u32(sV), ones0 = smem_u32(ones);
@@ -656,12 +679,12 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             if (++npf < count) pf.next(a);
         };
         while (npf < count && npf < kTrAhead) fetch();
-        for (int c = 0; c < count && ok; ++c) {
+        for (int c = 0; c < count; ++c) {
             if (npf < count) fetch();
             const int b = c & 1, pb = np == 2 ? b : 0;
-            if (fresh && seg++ > 0 && !mbar_wait(o_empty, (uint32_t)((seg - 2) & 1))) { ok = false; break; }
-            if (!mbar_wait(&v_full[b], (uint32_t)((c >> 1) & 1))) { ok = false; break; }
-            if (!mbar_wait(&p_full[b], (uint32_t)((c >> 1) & 1))) { ok = false; break; }
+            if (fresh && seg++ > 0) tr_wait(o_empty, (uint32_t)((seg - 2) & 1), limit);
+            tr_wait(&v_full[b], (uint32_t)((c >> 1) & 1), limit);
+            tr_wait(&p_full[b], (uint32_t)((c >> 1) & 1), limit);
             tc_fence_after();
             if (tr_elect()) {
 #pragma unroll
@@ -680,6 +703,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             __syncwarp();
             fresh = c + 1 < count && it.next(a);
         }
+        if (tr_elect()) mma_commit(&drained[1]);
+        mbar_wait(&drained[1], 0);
     } else if (count > 0 && warp < SW) {
         // ------------------------------------------------------------ softmax
         const int wg = warp >> 2, cb = wg * 32, wt = tid & 127, bar = 1 + wg;     // rows cb .. cb + 31
@@ -692,7 +717,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
         float cq = 0.0f;                                        // the chunk's factor; -1: its rows have their own
         bool fresh = true;
         uint32_t use = 0;                                       // votes so far
-        for (int c = 0; c < count; ++c) {                       // every item and barrier also after a wait has expired
+        for (int c = 0; c < count; ++c) {
             const bool start = fresh;
             if (start) {
                 const float fr = a.wsC[(it.g * a.rbs + it.rb) * NB + cb + lane];
@@ -722,7 +747,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                 fresh = it.next(a);
                 gn = r < it.left ? __ldg(gsrc + it.row + r) : (uint16_t)0;
             }
-            if (ok && !mbar_wait(&s_full[c & 1], (uint32_t)((c >> 1) & 1))) ok = false;
+            tr_wait(&s_full[c & 1], (uint32_t)((c >> 1) & 1), limit);
             tc_fence_after();
             uint32_t sr[32], w[16];                             // scores, then exponents; fp16 weights of row pairs
             // Exponents (s - Q) gg + (8 - ref) (at the start of a segment: before any reference) and their maximum.  The
@@ -772,8 +797,8 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) tr_arrive(&vote[wg]);
                 weights();
-                if (ok && !mbar_wait(&vote[wg], (use - 1) & 1)) ok = false;
-                slow = flag[2 * wg + (use & 1)] == use;
+                tr_vote_wait(&vote[wg], (use - 1) & 1);
+                slow = __any_sync(0xffffffffu, flag[2 * wg + (use & 1)] == use);
             }
             if (slow) {
                 // new references: the maxima over the tile's tokens
@@ -798,7 +823,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
                 for (int j = 0; j < 32; ++j) sr[j] = __float_as_uint(__uint_as_float(sr[j]) + sX[4 * NB + cb + j]);
                 weights();
                 if (!start) {                                   // O and the sums of the segment's earlier tiles
-                    if (ok && !pv_wait(c - 1)) ok = false;
+                    pv_wait(c - 1);
                     tc_fence_after();
                     const uint32_t at = tO + (uint32_t)cb + lanes;
                     tmem_ld32(at, t);
@@ -818,7 +843,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             tc_fence_before();                                  // the scores are read
             __syncwarp();
             if (lane == 0) tr_arrive(&s_empty[c & 1]);
-            if (c >= np && ok && !pv_wait(c - np)) ok = false;  // the tile whose weights lie in the buffer
+            if (c >= np) pv_wait(c - np);  // the tile whose weights lie in the buffer
             // row r of the [token][row] operand
             const uint32_t Pr = sP0 + (np == 2 ? (uint32_t)(c & 1) * (uint32_t)tr_pbytes(NB) : 0u) +
                                 (uint32_t)(cb >> 6) * (kTrTok * 128u) + (uint32_t)r * 128u;
@@ -830,7 +855,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             __syncwarp();
             if (lane == 0) tr_arrive(&p_full[c & 1]);
             if (fresh || c + 1 == count) {                      // end of the segment
-                if (ok && !pv_wait(c)) ok = false;
+                pv_wait(c);
                 tc_fence_after();
                 float *part = a.part + (size_t)(blockIdx.x + pg) * tr_part_floats(NB);
                 tmem_ld32(tO + (uint32_t)cb + lanes, sr);

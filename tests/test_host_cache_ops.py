@@ -2,6 +2,8 @@
 against their formulas (no GPU)."""
 import ctypes as C
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -237,3 +239,19 @@ def test_tree_binding_checks_shapes():
             bad()
     with pytest.raises(TypeError):
         f(q=q.half())
+
+
+def test_tree_kernel_takes_the_same_way_after_an_expired_wait():
+    """Every wait between the roles of the tree kernel has a limit, and none of them decides what a warp does next: a
+    warp that went another way after an expired wait would leave its group's barriers, which have no limit, for good."""
+    with open(os.path.join(os.path.dirname(L.LIB_PATH), "csrc", "qjl_tree.cuh")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    kernel = text[text.index("tree_attention_kernel("):text.index("tree_prologue_kernel(")]
+    roles = kernel[kernel.index("tr_wait_previous();"):kernel.rindex("__syncthreads();")]
+    assert re.search(r"void tr_wait\(uint64_t \*bar, uint32_t parity, uint32_t &limit\)", text)
+    assert re.search(r"void tr_vote_wait\(", text)             # neither has an answer
+    assert "break" not in roles and "__syncthreads" not in roles and "try_wait" not in roles
+    # the remaining ones: the last copy and products of the issuing warps, whose answer is not looked at
+    assert re.findall(r"(.*)\bmbar_wait(?:_limit)?\((.*?),", roles) == [
+        ("        if (loads > 0) ", "q_full"), ("        ", "&drained[0]"), ("        ", "&drained[1]")]
+    assert len(re.findall(r"\blimit\b", roles)) == len(re.findall(r", limit\)", roles)) + 3    # its start, the copies
