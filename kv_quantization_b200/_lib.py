@@ -9,6 +9,7 @@ missing or unloadable librq.so raises immediately -- there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import struct
 import threading
@@ -323,6 +324,35 @@ def _call(name, t, stream, args):
         raise RQError(name, status)
 
 
+@functools.lru_cache(None)
+def _types():
+    """The dtypes of fp32 arrays, int32 arrays, fp16 norms (or their bits) and projection matrices."""
+    import torch
+    return (torch.float32,), (torch.int32,), (torch.float16, torch.int16, torch.uint16), (torch.bfloat16, torch.float16)
+
+
+def _need(fn, index, *arrays):
+    """Refuse arrays that a kernel would misread or leave.  Each (tensor, types, bytes, name), if it is given, has to be of
+    one of the types (None: any), contiguous, of at least that many bytes, and on GPU `index`."""
+    for t, types, size, _ in arrays:
+        if t is not None and (t.nbytes < size or t.get_device() != index or not t.is_contiguous() or
+                              (types is not None and t.dtype not in types)):
+            break
+    else:
+        if index >= 0:
+            return
+    for t, types, size, name in arrays:
+        if t is not None and types is not None and t.dtype not in types:
+            raise TypeError(f"{fn}: {name}: expected {' or '.join(map(str, types))}, got {t.dtype}")
+        if t is not None and (not t.is_contiguous() or t.nbytes < size):
+            raise ValueError(f"{fn}: {name}: expected a contiguous tensor of at least {size} bytes")
+    _other_device(fn)
+
+
+def _other_device(fn):
+    raise ValueError(f"{fn}: expected all tensors on one GPU")
+
+
 _pack3 = struct.Struct("3q").pack
 
 
@@ -339,6 +369,14 @@ def _host(a, dtype):
     if type(a) is not np.ndarray or a.dtype != dtype:
         a = np.asarray(a, dtype=dtype)
     return a.tobytes()
+
+
+def _levels(fn, centroids, bits):
+    """The bytes of a host table of 2^bits centroids."""
+    table = _host(centroids, np.float32)
+    if 1 <= bits <= 8 and len(table) < 4 << bits:
+        raise ValueError(f"{fn}: table of {1 << bits} centroids expected")
+    return table
 
 
 def rq_rotary_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = RQ_ROPE_PLAIN, factor: float = 1.0,
@@ -370,9 +408,14 @@ def rq_rotary(x, out, positions, freq, rot_dim, style, scale=1.0, inverse=False,
         H2, p2 = shape2[2], (x2.data_ptr(), _strides(x2, "x2"), out2.data_ptr(), _strides(out2, "out2"))
     if out.dtype != x.dtype:
         raise TypeError("rq_rotary: out has another dtype than x")
+    dtype, xs, ost = _dtype_code(x), _strides(x, "x"), _strides(out, "out")
+    index = x.get_device()
+    if index < 0 or out.get_device() != index or positions.get_device() != index or \
+            (x2 is not None and (x2.get_device() != index or out2.get_device() != index)):
+        _other_device("rq_rotary")
     _call("rq_rotary", x, stream, (
-        x.data_ptr(), _strides(x, "x"), out.data_ptr(), _strides(out, "out"), H, *p2, H2, _dtype_code(x), B, n, d,
-        rot_dim, style, positions.data_ptr(), ps[0], f, scale, 1 if inverse else 0))
+        x.data_ptr(), xs, out.data_ptr(), ost, H, *p2, H2, dtype, B, n, d, rot_dim, style, positions.data_ptr(), ps[0], f,
+        scale, 1 if inverse else 0))
 
 
 def rq_evict_accumulate_workspace_bytes(G, n_q, T) -> int:
@@ -380,27 +423,43 @@ def rq_evict_accumulate_workspace_bytes(G, n_q, T) -> int:
 
 
 def rq_evict_accumulate(scores, G, n_q, T, softmax_scale, decay, acc, out, workspace, row_len=None, stream=None):
-    """out [G][T] = decay * acc + sum over queries of softmax(softmax_scale * scores [G][n_q][T])."""
+    """out [G][T] = decay * acc + sum over queries of softmax(softmax_scale * scores [G][n_q][T]); all fp32, row_len
+    int32 [G][n_q]."""
+    float32, int32, _, _ = _types()
+    _need("rq_evict_accumulate", out.get_device(), (out, float32, 4 * G * T, "out"), (scores, float32, 4 * G * n_q * T, "scores"),
+          (acc, float32, 4 * G * T, "acc"), (row_len, int32, 4 * G * n_q, "row_len"), (workspace, None, 0, "workspace"))
     _call("rq_evict_accumulate", out, stream, (
         _ptr(scores), G, n_q, T, _ptr(row_len), softmax_scale, decay, _ptr(acc), out.data_ptr(), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size()))
 
 
 def rq_evict_select(acc, G, T, keep, idx, count, length=None, n_sink=0, n_recent=0, stream=None):
-    """idx int32 [G][keep]: the tokens to keep of each group, ascending, then -1; count int32 [G]."""
+    """idx int32 [G][keep]: the tokens to keep of each group by acc fp32 [G][T], ascending, then -1; count int32 [G];
+    length int32 [G]."""
+    float32, int32, _, _ = _types()
+    _need("rq_evict_select", idx.get_device(), (idx, int32, 4 * G * keep, "idx"), (count, int32, 4 * G, "count"),
+          (acc, float32, 4 * G * T, "acc"), (length, int32, 4 * G, "length"))
     _call("rq_evict_select", idx, stream, (_ptr(acc), G, T, _ptr(length), keep, n_sink, n_recent, idx.data_ptr(),
                                            count.data_ptr()))
 
 
 def rq_evict_gather(idx, count, G, keep, T, arrays, T_dst=None, stream=None):
-    """Move the records idx [G][keep] of every (src [G][T]..., dst [G][T_dst]...) pair of contiguous tensors."""
+    """Move the records idx (int32 [G][keep]), count (int32 [G]) of every (src [G][T]..., dst [G][T_dst]...) pair of
+    contiguous tensors."""
+    int32 = _types()[1]
     T_dst = keep if T_dst is None else T_dst
-    rows = []
+    rows, index, here = [], idx.get_device(), True
     for src, dst in arrays:
-        size = src.numel() * src.element_size() // max(1, G * T)
-        if dst.numel() * dst.element_size() != size * G * T_dst:
-            raise ValueError("rq_evict_gather: dst does not hold [G][T_dst] records of src's size")
+        have, room, size = src.nbytes, dst.nbytes, 0
+        if G * T:
+            size = have // (G * T)
+        elif G * T_dst:                                        # nothing to move
+            size = room // (G * T_dst)
+        if have != size * G * T or room != size * G * T_dst or not src.is_contiguous() or not dst.is_contiguous():
+            raise ValueError("rq_evict_gather: expected contiguous src [G][T] and dst [G][T_dst] of records of one size")
+        here = here and src.get_device() == index and dst.get_device() == index
         rows += (src.data_ptr(), dst.data_ptr(), size)
+    _need("rq_evict_gather", index if here else -1, (idx, int32, 4 * G * keep, "idx"), (count, int32, 4 * G, "count"))
     _call("rq_evict_gather", idx, stream, (idx.data_ptr(), count.data_ptr(), G, keep, T, T_dst,
                                            struct.pack(f"{len(rows)}q", *rows), len(arrays)))
 
@@ -414,8 +473,10 @@ def qjl_tree_attention(q, k_new, v_new, tree_mask, m, proj, signs, sk_norms, T, 
                        layout=RQ_CODES_PACKED, use_signs=0, sign_seed=0, centroids=None, v_layout=RQ_CODES_PACKED,
                        v_use_signs=0, v_sign_seed=0, stream=None):
     """Attention of drafted tokens q [B, n_nodes, heads, d] over the compressed cache and over k_new, v_new
-    [B, n_nodes, kv_heads, d]; tree_mask int64 [B or 1, n_nodes, words] (None: a chain); out bf16 of q's shape."""
+    [B, n_nodes, kv_heads, d]; tree_mask int64 [B or 1, n_nodes, words] (None: a chain); kv_len int32 [B * kv_heads];
+    out bf16 of q's shape."""
     import torch
+    fn = "qjl_tree_attention"
     shape, kshape = q.shape, k_new.shape
     B, n, H, d = shape
     kv = kshape[2]
@@ -428,15 +489,24 @@ def qjl_tree_attention(q, k_new, v_new, tree_mask, m, proj, signs, sk_norms, T, 
     if tree_mask is not None:
         ms = tree_mask.shape
         if len(ms) != 3 or ms[0] not in (1, B) or ms[1] != n or ms[2] != (n + 63) // 64 or \
-                tree_mask.element_size() != 8 or not tree_mask.is_contiguous():
+                tree_mask.dtype not in (torch.int64, torch.uint64) or not tree_mask.is_contiguous():
             raise ValueError("qjl_tree_attention: contiguous 64-bit tree_mask [B or 1, n_nodes, ceil(n_nodes / 64)] expected")
         stride = n * ms[2] if ms[0] > 1 else 0
-    c = None if centroids is None else _host(centroids, np.float32)
-    vc = _host(v_centroids, np.float32)
+    strides = _strides(q, "q"), _strides(k_new, "k_new"), _strides(v_new, "v_new"), _strides(out, "out")
+    _, int32, half, proj16 = _types()
+    rows, kw, vw = B * kv * T, 8 if layout == RQ_CODES_INT8 else bits, 8 if v_layout == RQ_CODES_INT8 else v_bits
+    index = q.get_device()
+    here = k_new.get_device() == index and v_new.get_device() == index and out.get_device() == index and \
+        (tree_mask is None or tree_mask.get_device() == index)
+    _need(fn, index if here else -1, (proj, proj16, 2 * m * d, "proj"), (signs, None, rows * m // 8, "signs"),
+          (sk_norms, half, 2 * rows, "sk_norms"), (kv_len, int32, 4 * B * kv, "kv_len"), (codes, None, rows * d * kw // 8, "codes"),
+          (norms, half, 2 * rows, "norms"), (v_codes, None, rows * d * vw // 8, "v_codes"), (v_norms, half, 2 * rows, "v_norms"),
+          (workspace, None, 0, "workspace"))
+    c = None if centroids is None else _levels(fn, centroids, bits)
+    vc = _levels(fn, v_centroids, v_bits)
     _call("qjl_tree_attention", q, stream, (
-        q.data_ptr(), _strides(q, "q"), k_new.data_ptr(), _strides(k_new, "k_new"), v_new.data_ptr(),
-        _strides(v_new, "v_new"), B, kv, H // kv, n, d, _ptr(tree_mask), stride, m, proj.data_ptr(), _dtype_code(proj),
-        _ptr(signs), _ptr(sk_norms), T, _ptr(kv_len), _ptr(codes), _ptr(norms), bits, layout, int(use_signs),
-        sign_seed, c, _ptr(v_codes), _ptr(v_norms), v_bits, v_layout,
-        int(v_use_signs), v_sign_seed, vc, softmax_scale, out.data_ptr(), _strides(out, "out"),
+        q.data_ptr(), strides[0], k_new.data_ptr(), strides[1], v_new.data_ptr(), strides[2], B, kv, H // kv, n, d,
+        _ptr(tree_mask), stride, m, proj.data_ptr(), _dtype_code(proj), _ptr(signs), _ptr(sk_norms), T, _ptr(kv_len),
+        _ptr(codes), _ptr(norms), bits, layout, int(use_signs), sign_seed, c, _ptr(v_codes), _ptr(v_norms), v_bits, v_layout,
+        int(v_use_signs), v_sign_seed, vc, softmax_scale, out.data_ptr(), strides[3],
         workspace.data_ptr(), workspace.numel() * workspace.element_size()))

@@ -255,3 +255,100 @@ def test_tree_kernel_takes_the_same_way_after_an_expired_wait():
     assert re.findall(r"(.*)\bmbar_wait(?:_limit)?\((.*?),", roles) == [
         ("        if (loads > 0) ", "q_full"), ("        ", "&drained[0]"), ("        ", "&drained[1]")]
     assert len(re.findall(r"\blimit\b", roles)) == len(re.findall(r", limit\)", roles)) + 3    # its start, the copies
+
+
+# ------------------------------------------------------------------ arrays that a kernel would misread or leave
+
+def zeros(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def call_accumulate(**kw):
+    a = dict(scores=zeros(2, 3, 8), acc=zeros(2, 8), out=zeros(2, 8), workspace=zeros(64, dtype=torch.uint8),
+             row_len=zeros(2, 3, dtype=torch.int32))
+    a.update(kw)
+    L.rq_evict_accumulate(a["scores"], 2, 3, 8, 1.0, 1.0, a["acc"], a["out"], a["workspace"], row_len=a["row_len"], stream=0)
+
+
+def call_select(**kw):
+    a = dict(acc=zeros(2, 8), idx=zeros(2, 4, dtype=torch.int32), count=zeros(2, dtype=torch.int32),
+             length=zeros(2, dtype=torch.int32))
+    a.update(kw)
+    L.rq_evict_select(a["acc"], 2, 8, 4, a["idx"], a["count"], length=a["length"], stream=0)
+
+
+def call_gather(**kw):
+    a = dict(idx=zeros(2, 4, dtype=torch.int32), count=zeros(2, dtype=torch.int32), src=zeros(2, 8, 3), dst=zeros(2, 4, 3))
+    a.update(kw)
+    L.rq_evict_gather(a["idx"], a["count"], 2, 4, 8, [(a["src"], a["dst"])], stream=0)
+
+
+def call_rotary(**kw):
+    x = zeros(2, 3, 4, 64, dtype=torch.bfloat16)
+    L.rq_rotary(x, x, zeros(2, 3, dtype=torch.int64), np.ones(32), 64, 0, stream=0, **kw)
+
+
+def call_tree(**kw):
+    B, n, kv, rep, m, T, d = 2, 3, 2, 2, 128, 10, 128
+    rows = B * kv * T
+    q, k = zeros(B, n, kv * rep, d, dtype=torch.bfloat16), zeros(B, n, kv, d, dtype=torch.bfloat16)
+    a = dict(proj=zeros(m, d, dtype=torch.bfloat16), signs=zeros(rows, m // 8, dtype=torch.uint8),
+             sk=zeros(rows, dtype=torch.int16), kv_len=zeros(B * kv, dtype=torch.int32),
+             v_codes=zeros(rows, 64, dtype=torch.uint8), v_norms=zeros(rows, dtype=torch.float16),
+             codes=zeros(rows, 32, dtype=torch.uint8), norms=zeros(rows, dtype=torch.float16), mask=None,
+             ws=zeros(64, dtype=torch.uint8), vc=L.rq_lloyd_max(4), kc=L.rq_lloyd_max(2))
+    a.update(kw)
+    L.qjl_tree_attention(q, k, k, a["mask"], m, a["proj"], a["signs"], a["sk"], T, a["kv_len"], a["v_codes"], a["v_norms"],
+                         4, a["vc"], q, a["ws"], 1.0, codes=a["codes"], norms=a["norms"], bits=2, centroids=a["kc"],
+                         stream=0)
+
+
+def odd(t):
+    """The same shape and values, in another order of memory."""
+    return t.transpose(0, -1).contiguous().transpose(0, -1)
+
+
+@pytest.mark.parametrize("call, name, bad, error", [
+    (call_accumulate, "out", zeros(2, 8, dtype=torch.float16), TypeError), (call_accumulate, "out", zeros(2, 7), ValueError),
+    (call_accumulate, "out", odd(zeros(2, 8)), ValueError),
+    (call_accumulate, "scores", zeros(2, 3, 8, dtype=torch.bfloat16), TypeError),
+    (call_accumulate, "scores", zeros(2, 2, 8), ValueError), (call_accumulate, "scores", odd(zeros(2, 3, 8)), ValueError),
+    (call_accumulate, "acc", zeros(2, 8, dtype=torch.float16), TypeError), (call_accumulate, "acc", zeros(1, 8), ValueError),
+    (call_accumulate, "row_len", zeros(2, 3, dtype=torch.int64), TypeError),
+    (call_accumulate, "row_len", zeros(2, dtype=torch.int32), ValueError),
+    (call_accumulate, "workspace", zeros(64, 2)[:, :1], ValueError),
+    (call_select, "acc", zeros(2, 8, dtype=torch.float64), TypeError), (call_select, "acc", zeros(2, 16)[:, ::2], ValueError),
+    (call_select, "idx", zeros(2, 4, dtype=torch.int64), TypeError), (call_select, "idx", zeros(2, 3, dtype=torch.int32), ValueError),
+    (call_select, "count", zeros(2, dtype=torch.int64), TypeError), (call_select, "count", zeros(1, dtype=torch.int32), ValueError),
+    (call_select, "length", zeros(2, dtype=torch.int64), TypeError), (call_select, "length", zeros(1, dtype=torch.int32), ValueError),
+    (call_gather, "idx", zeros(2, 4, dtype=torch.int64), TypeError), (call_gather, "idx", zeros(7, dtype=torch.int32), ValueError),
+    (call_gather, "count", zeros(2, dtype=torch.int64), TypeError), (call_gather, "src", odd(zeros(2, 8, 3)), ValueError),
+    (call_gather, "src", zeros(2, 7, 3), ValueError), (call_gather, "dst", odd(zeros(2, 4, 3)), ValueError),
+    (call_tree, "proj", zeros(128, 128), TypeError), (call_tree, "proj", zeros(64, 128, dtype=torch.bfloat16), ValueError),
+    (call_tree, "signs", odd(zeros(40, 16, dtype=torch.uint8)), ValueError), (call_tree, "signs", zeros(39, 16, dtype=torch.uint8), ValueError),
+    (call_tree, "sk", zeros(40), TypeError), (call_tree, "sk", zeros(39, dtype=torch.int16), ValueError),
+    (call_tree, "kv_len", zeros(4, dtype=torch.int64), TypeError), (call_tree, "kv_len", zeros(2, dtype=torch.int32), ValueError),
+    (call_tree, "v_codes", zeros(40, 32, dtype=torch.uint8), ValueError),
+    (call_tree, "v_codes", odd(zeros(40, 64, dtype=torch.uint8)), ValueError),
+    (call_tree, "v_norms", zeros(40), TypeError), (call_tree, "v_norms", zeros(20, dtype=torch.float16), ValueError),
+    (call_tree, "codes", zeros(40, 16, dtype=torch.uint8), ValueError), (call_tree, "norms", zeros(40), TypeError),
+    (call_tree, "norms", zeros(40, dtype=torch.bfloat16), TypeError),
+    (call_tree, "mask", zeros(2, 3, 1, dtype=torch.float64), ValueError), (call_tree, "ws", zeros(64, 2)[:, :1], ValueError),
+    (call_tree, "vc", L.rq_lloyd_max(3), ValueError), (call_tree, "kc", L.rq_lloyd_max(1), ValueError),
+])
+def test_binding_refuses_arrays_of_other_types_sizes_and_orders(call, name, bad, error):
+    with pytest.raises(error, match="expected"):
+        call(**{name: bad})
+
+
+@pytest.mark.parametrize("call", [call_accumulate, call_select, call_gather, call_rotary, call_tree])
+def test_binding_refuses_tensors_that_are_not_on_a_gpu(call):
+    """Tensors that are right but for the memory they lie in: their addresses mean nothing to a kernel."""
+    with pytest.raises(ValueError, match="on one GPU"):
+        call()
+
+
+def test_gather_of_an_empty_cache_is_a_noop_for_the_library():
+    rows = (L.Rows * 1)()
+    rows[0].src, rows[0].dst, rows[0].row_bytes = A, A + 0x1000, 12
+    assert L.lib().rq_evict_gather(A, A, 2, 4, 0, 4, C.addressof(rows), 1, None) == 0
