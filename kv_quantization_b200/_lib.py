@@ -306,20 +306,20 @@ def _ptr(t):
 
 
 def _call(name, t, stream, args):
-    """Call `name` with `args` and a stream; without one, the current stream of the device of tensor `t`, also when
-    another device is current."""
+    """Call `name` with `args` on the device of tensor `t`, also when another device is current, and on `stream`: that
+    device's current one, if none is given."""
+    import torch
     fn = getattr(_lib or lib(), name)
-    if stream is not None:
-        status = fn(*args, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    else:
-        import torch
-        index, current = t.get_device(), torch._C._cuda_getDevice()
+    index = t.get_device()
+    if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
-        if index == current:
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
             status = fn(*args, raw)
-        else:
-            with torch.cuda.device(index):
-                status = fn(*args, raw)
     if status != 0:
         raise RQError(name, status)
 

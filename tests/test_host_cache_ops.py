@@ -352,3 +352,29 @@ def test_gather_of_an_empty_cache_is_a_noop_for_the_library():
     rows = (L.Rows * 1)()
     rows[0].src, rows[0].dst, rows[0].row_bytes = A, A + 0x1000, 12
     assert L.lib().rq_evict_gather(A, A, 2, 4, 0, 4, C.addressof(rows), 1, None) == 0
+
+
+@pytest.mark.parametrize("stream, raw", [(None, 77), (5, 5), (type("S", (), {"cuda_stream": 9}), 9)])
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch, stream, raw, current):
+    """Also when another device is current and a stream is given: the legacy stream of the current device would run the
+    kernel there, on addresses of another device."""
+    state, seen = dict(device=current), []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, state["device"] = state["device"], self.index
+
+        def __exit__(self, *exc):
+            state["device"] = self.before
+
+    fake = type("Lib", (), {"rq_evict_select": staticmethod(lambda *a: seen.append((state["device"], a)) or 0)})
+    monkeypatch.setattr(L, "_lib", fake)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["device"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: {1: 77}[i], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    L._call("rq_evict_select", type("T", (), {"get_device": staticmethod(lambda: 1)}), stream, ("x",))
+    assert seen == [(1, ("x", raw))] and state["device"] == current
