@@ -241,6 +241,30 @@ def test_gather(G, T, keep):
         assert torch.equal(d[:1] if w > 3 else d, want[:1] if w > 3 else want)
 
 
+@pytest.mark.parametrize("G,T,keep", [(33, 5001, 4099), (3, 70001, 50021), (1, 131072, 131072)])
+def test_gather_of_long_caches(G, T, keep):
+    """keep * G of 2^17 and more (256 rows a block) with a remainder, every group, in each width of access."""
+    assert keep * G >= 256 * 512
+    g = torch.Generator(device=DEV)
+    g.manual_seed(keep)
+    widths = (1, 2, 3, 4, 8, 24, 32, 48, 64)
+    src = [torch.randint(0, 256, (G, T, w), generator=g, device=DEV, dtype=torch.uint8) for w in widths]
+    T_dst = keep + 5
+    dst = [torch.full((G, T_dst, w), 9, device=DEV, dtype=torch.uint8) for w in widths]
+    idx = torch.stack([torch.randperm(T, generator=g, device=DEV)[:keep].sort().values for _ in range(G)]).int()
+    count = torch.randint(0, keep + 1, (G,), generator=g, device=DEV, dtype=torch.int32)
+    count[0] = keep
+    outside = torch.rand(G, keep, generator=g, device=DEV) < 0.01
+    idx = torch.where(outside, torch.where(idx % 2 == 0, -idx - 1, idx + T), idx)
+    L.rq_evict_gather(idx, count, G, keep, T, list(zip(src, dst)), T_dst=T_dst)
+    live = (torch.arange(keep, device=DEV) < count[:, None]) & ~outside
+    rows = torch.where(live, idx, 0).long()[..., None]
+    for s, d, w in zip(src, dst, widths):
+        want = torch.full_like(d, 9)
+        want[:, :keep] = torch.where(live[..., None], torch.gather(s, 1, rows.expand(-1, -1, w)), want[:, :keep])
+        assert torch.equal(d, want), f"width {w}"
+
+
 def test_gather_far_offsets():
     """Records past 2^32 bytes; the same index twice."""
     T = (1 << 32) // 512 + 100

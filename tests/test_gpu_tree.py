@@ -451,3 +451,23 @@ def test_values_of_every_size(n, rep, vbits, size, table):
     got = run(c, q, kn, vn, None, m, T, None, 0, vbits, 0.3)
     kt, vt = vectors(c, 1, T, m, 0, vbits)
     check(got, kt, vt, q, kn, vn, None, None, 0.3)
+
+
+@pytest.mark.parametrize("rows,m,kbits,vbits", [(128, 256, 2, 4), (64, 512, 4, 4), (32, 256, 2, 4), (16, 512, 0, 4), (48, 512, 4, 3)])
+def test_single_buffers_are_used_again(rows, m, kbits, vbits):
+    """Shapes whose operand and tables leave room for one weight buffer and one value buffer (or for one CTA an SM), with
+    tens of tiles a CTA."""
+    B, KV, T = 24, 2, 20011
+    c = compress(B * KV, T, D, m, kbits, vbits, 500 + rows, kbits > 0)
+    q, kn, vn = drafted(B, rows, KV, 1, 200 + rows)
+    lens = torch.tensor([T - 97 * i for i in range(B * KV)], dtype=torch.int32, device=DEV)
+    scale = 1 / math.sqrt(D)
+    got = run(c, q, kn, vn, None, m, T, lens, kbits, vbits, scale)
+    torch.cuda.synchronize()
+    assert L.rq_device_error(True) == 0
+    for b in (0, 11, B - 1):
+        part = {k: (v[b * KV * (v.shape[0] // (B * KV)):(b + 1) * KV * (v.shape[0] // (B * KV))]
+                    if isinstance(v, torch.Tensor) and k not in ("k", "v", "S") else v) for k, v in c.items()}
+        kt, vt = vectors(part, KV, T, m, kbits, vbits)
+        check(got[b:b + 1], kt, vt, q[b:b + 1], kn[b:b + 1], vn[b:b + 1], None, lens[b * KV:(b + 1) * KV], scale)
+    assert torch.equal(got, run(c, q, kn, vn, None, m, T, lens, kbits, vbits, scale))
