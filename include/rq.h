@@ -347,7 +347,8 @@ rq_status rq_rotary_frequencies(int rot_dim, double theta, rq_rope_scaling scali
  *   same strides (in place), else they must not overlap.  Writing with other
  *   strides lays the keys out per head for rq_quantize / qjl_sketch.
  *   positions: DEVICE int64, batch b at positions + b * pos_batch_stride (0: shared
- *   by the batch); any value, the angle is reduced exactly (64-bit fixed-point turns).
+ *   by the batch); any value: the angle is reduced in 64-bit fixed-point turns, with an
+ *   error of at most 2^-32 + |position| (1 + |freq|) 2^-65 turns (at 2^40: 2^-25).
  *   freq: HOST, rot_dim / 2 finite float64 (rq_rotary_frequencies, or any).
  *   d even, 2 .. 512; rot_dim even, 2 .. d; |freq| < 2^20.
  * Computed in fp32, rounded once. */
@@ -380,8 +381,18 @@ rq_status rq_rotary(const void *x, const rq_strides *x_strides, void *out, const
  *   clamped to 0 .. T, or NULL: T.  T = 0: the cache pointers may be NULL.
  *   workspace: qjl_tree_attention_workspace_bytes(...) bytes (overwritten); calls
  *   (or captured graphs) that may run at the same time need one each.
- * Arithmetic as qjl_attention; the drafted part, sums and joins in fp32; the
- * output is rounded once.
+ * Arithmetic: fp32, with fp16 operands of the tensor cores where the cache is read:
+ *   queries   [H D q ; S q] times a power of two, 2^-e of the largest element of the
+ *             row (or of its 32 neighbours' largest, where all are within 2^4);
+ *   keys      centroids and +-rho as in qjl_score;
+ *   weights   2^(a - r + 8), a the logit in units of log2 and r a running reference
+ *             that is at most 7 below the maximum: a weight under 2^-22 of the
+ *             reference's rounds like an fp16 subnormal, by 2^-33 of it at most;
+ *   values    c 2^-e, 2^e just above max |c|, and its product with the norm n, each
+ *             rounded to fp16: by 2^-11 of itself, or by 2^-25 where it is below 2^-14.
+ * (qjl_attention rounds c and n / d to fp16 and scales weights by 2^14 of the true
+ * running maximum: the two agree to these roundings, not bit for bit.)  The
+ * drafted part, sums and joins are fp32; the output is rounded once.
  * Supported: d = 128, m % 64 == 0, codes of 1, 2, 3, 4 bits packed or int8, values
  * likewise (RQ_EUNSUPPORTED otherwise); n_nodes <= 1024. */
 
@@ -402,9 +413,13 @@ rq_status qjl_tree_attention(const void *q, const rq_strides *q_strides, const v
 /* ---- Eviction by accumulated attention weight --------------------------------
  * Keep the cached tokens that received the most attention: add each step's
  * softmax weights (of qjl_score's scores) to a sum per token, choose the tokens
- * with the largest sums, move their records together. */
+ * with the largest sums, move their records together.  The weights are normalised
+ * over the scores that are given, the cached tokens: qjl_tree_attention's also run
+ * over the drafted ones, so its weight of a cached token is smaller by the cached
+ * tokens' share of that softmax. */
 
-/* Device workspace rq_evict_accumulate needs (bytes). */
+/* Device workspace rq_evict_accumulate needs (bytes); overwritten, so calls (or
+ * captured graphs) that may run at the same time need one each. */
 size_t rq_evict_accumulate_workspace_bytes(int64_t G, int n_q, int64_t T);
 
 /* out[g][t] = decay * acc[g][t] + sum over the group's n_q queries of

@@ -9,8 +9,9 @@ namespace {
 
 int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
-// Query rows a block: 32 or 64 when that holds the group's rows; above, 128 (fewer passes over the cache: 256 rows in
-// blocks of 128 397 us, of 64 482 us, of 32 732 us) where the operand of kb columns leaves room in shared memory.
+// Query rows a block: 32 or 64 when that holds the group's rows; above, 128 (fewer passes over the cache) where the
+// operand of kb columns leaves room in shared memory.  Measured over 32 x 32768 tokens: 128 rows on two-stage keys in
+// blocks of 128 317 us, of 64 366 us, of 32 629 us; 256 rows on pure sketch keys 420, 416 and 672 us.
 int tree_nb(int rows, int kb) { return rows <= 32 ? 32 : (rows <= 64 || kb > 384 ? 64 : 128); }
 
 int64_t tree_grid(int64_t G, int rbs, int nb, int64_t T, int num_sms)

@@ -27,11 +27,12 @@
 //                        weights are computed, and no reduction over tokens.
 //   MMA 2 (one thread)   O^T[d][row] += V'^T . P and the rows' weight sums P^T . 1, in TMEM over the segment.
 //
-// Measured (B200): 32 rows x 32 groups x 32768 tokens, m = 256, 4-bit values: 113 us whole (105 MB: 16 us at the copy
-// rate; 26 GFLOP of score and value products: 16 us); 256 rows: 397 us (206 GFLOP: 125 us).  What bounds it: neither
-// memory (DRAM 8 %) nor the tensor pipe (11 and 24 %), but the instructions around them, about 7000 a 128-token tile of
-// 32 rows at 0.44 issued per scheduler and cycle: unpacking (1800), weights (900), and the waits, address arithmetic and
-// barriers of the roles.
+// Measured (B200): 32 rows x 32 groups x 32768 tokens, m = 256, 4-bit values: 104 us whole (105 MB: 16 us at the copy
+// rate; 26 GFLOP of score and value products: 16 us); 256 rows: 414 us (206 GFLOP: 125 us).  What bounds it: neither
+// memory (DRAM 10 %) nor the tensor pipe (13 and 25 %) nor the issue of instructions (0.46 and 0.40 a scheduler and
+// cycle), but exposed latency: the first stall is a load (long_scoreboard: a producer's own token's records from L2, a
+// softmax warp's scores from tensor memory), with too few warps to cover it.  Up to 32 rows the single weight and value
+// buffer adds to it; at 256 rows the softmax warps are the critical path.
 #pragma once
 #include "rq_cache_ops.h"
 #include "rq_common.cuh"
@@ -46,17 +47,18 @@ constexpr float kTrShift = 8.0f;                  // weight of the reference: 2^
 constexpr float kTrMost = 15.0f;                  // largest exponent an fp16 weight may have
 // The score operand of a row in fp16 is [H D q ; S q] 2^-e / 16, 2^e <= max |q_i| < 2^(e + 1): at most |S_i| sqrt(2), and
 // for a pure sketch times 2 .. 2^-7 (tr_bit_factor).  Rows of a chunk of 32 whose e are within kTrSpread share the
-// largest: the smallest of them still lies 2^-13 high where S is N(0, 1) and a half step of fp16 is 2^-25, as precise as
-// a normal fp16 value.  In a chunk with a wider spread every row has its own e, and the softmax multiplies by it.
+// largest: with S of N(0, 1) the coordinates of a row of N(0, 1) values that is 2^-4 of it are still 2^-13 at that
+// smallest factor, where half a step of fp16, 2^-25, is as small a part as for a normal value.  In a chunk with a wider
+// spread every row has its own e, and the softmax multiplies by it (32 rows x 32 x 32768 tokens: 117 us instead of 111).
 constexpr int kTrSpread = 4;
 constexpr float kTrRowScale = 16.0f;
 
 constexpr int kTrAhead = 4;                       // tiles that the cache's records are prefetched into L2 ahead
 
 // Warps of a CTA: NB / 32 groups of four softmax warps (a group has 32 rows), groups of four producer warps (with two,
-// a group unpacks every second tile), two issuing warps.  Measured at 32 rows: one producer group in each of two CTAs
-// an SM 137 us, two groups 146 us (spills at 72 registers), one CTA 197 us; at 128: one group 476 us, two 494 us; at 64
-// two groups 52 us, one 62 us.
+// a group unpacks every second tile), two issuing warps.  Measured (32 groups x 32768 tokens, pure sketch keys): at 32
+// rows one producer group in each of two CTAs an SM 111 us, two groups 115 us (spills at 72 registers); at 64 two groups
+// 127 us, one 163 us; at 256 one group 420 us, two 435 us.
 __host__ __device__ constexpr int tr_softmax_warps(int nb) { return nb / 8; }
 __host__ __device__ constexpr int tr_producer_groups(int nb) { return nb == 64 ? 2 : 1; }
 __host__ __device__ constexpr int tr_threads(int nb) { return (tr_softmax_warps(nb) + 4 * tr_producer_groups(nb) + 2) * 32; }
@@ -65,8 +67,8 @@ __host__ __device__ constexpr int tr_ctas(int nb) { return nb == 32 ? 2 : 1; }
 __host__ __device__ constexpr int tr_sbufs(int nb) { return nb == 128 ? 1 : 2; }
 __host__ __device__ constexpr int tr_kslots(int nb) { return nb == 32 ? 4 : nb == 64 ? 8 : 6; }
 __host__ __device__ constexpr int tr_tmem(int nb) { return nb == 32 ? 256 : 512; }
-// log2 of the copies of the value and key lookup tables: 32 copies have no bank conflicts (values with 8: 124 us, 16: 118,
-// 32: 113 at 32 rows); the keys' have fewer where shared memory is short.
+// log2 of the copies of the value and key lookup tables: 32 copies have no bank conflicts (values with 8: 117 us, 16: 115,
+// 32: 111 at 32 rows; 430, 424, 420 at 256); the keys' have fewer where shared memory is short.
 __host__ __device__ constexpr int tr_vcl(int) { return 5; }
 __host__ __device__ constexpr int tr_kcl(int nb) { return nb == 64 ? 5 : 3; }
 __host__ __device__ inline size_t tr_pbytes(int nb) { return (size_t)(nb > 64 ? 2 : 1) * kTrTok * 128; }
@@ -371,8 +373,8 @@ __device__ __forceinline__ void tr_load_codes(const uint8_t *p, int pw, bool val
     }
 }
 
-// V4: values of 4 bits (fewer and wider loads, no choice of width in the loop: 137 -> 124 us at 32 rows x 32 x 32768
-// tokens, 476 -> 458 us at 256 rows).
+// V4: values of 4 bits (fewer and wider loads, no choice of width in the loop: 127 -> 111 us at 32 rows x 32 x 32768
+// tokens, 143 -> 127 us at 64, 428 -> 420 us at 256).
 template <int NB, bool TWO, bool V4>
 __global__ void __launch_bounds__(tr_threads(NB), tr_ctas(NB))
 tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ QuantTables TK,
@@ -752,7 +754,7 @@ tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant_
             uint32_t sr[32], w[16];                             // scores, then exponents; fp16 weights of row pairs
             // Exponents (s - Q) gg + (8 - ref) (at the start of a segment: before any reference) and their maximum.  The
             // scores stay in TMEM until the vote is known: held in registers for the unusual answer they spill (256 rows:
-            // 444 us instead of 397).
+            // 12 % slower).
             auto exponents = [&]() {
                 tmem_ld32(tS + (uint32_t)(c % NS * NB + cb) + lanes, sr);
                 tmem_ld_wait();

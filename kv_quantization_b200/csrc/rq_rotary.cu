@@ -5,8 +5,9 @@
 // head are copied.  The transpose (sin -> -sin) is the inverse rotation times scale^2: the gradient.
 //
 // Angles are kept in turns as 64-bit fixed point: position * F mod 2^64, F = round(freq / 2 pi * 2^64), is the
-// angle modulo a full turn with no cancellation at any position (an error of position * 2^-65 turns), so a far
-// position costs one integer multiply instead of a float64 range reduction; its top 32 bits go to sincospif.
+// angle modulo a full turn with no cancellation at any position (an error of |position| (1 + freq) 2^-65 turns from
+// rounding F), so a far position costs one integer multiply instead of a float64 range reduction; its top 32 bits go to
+// sincospif.
 //
 // Bound by HBM: every value is read and written once.  A CTA takes a few tokens; their cosines and sines are
 // computed once into shared memory and then used for all heads (the angle does not depend on the head), each
