@@ -427,7 +427,7 @@ def rq_evict_accumulate(scores, G, n_q, T, softmax_scale, decay, acc, out, works
     int32 [G][n_q]."""
     float32, int32, _, _ = _types()
     _need("rq_evict_accumulate", out.get_device(), (out, float32, 4 * G * T, "out"), (scores, float32, 4 * G * n_q * T, "scores"),
-          (acc, float32, 4 * G * T, "acc"), (row_len, int32, 4 * G * n_q, "row_len"), (workspace, None, 0, "workspace"))
+          (acc if decay else None, float32, 4 * G * T, "acc"), (row_len, int32, 4 * G * n_q, "row_len"), (workspace, None, 0, "workspace"))
     _call("rq_evict_accumulate", out, stream, (
         _ptr(scores), G, n_q, T, _ptr(row_len), softmax_scale, decay, _ptr(acc), out.data_ptr(), _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size()))

@@ -267,7 +267,7 @@ def call_accumulate(**kw):
     a = dict(scores=zeros(2, 3, 8), acc=zeros(2, 8), out=zeros(2, 8), workspace=zeros(64, dtype=torch.uint8),
              row_len=zeros(2, 3, dtype=torch.int32))
     a.update(kw)
-    L.rq_evict_accumulate(a["scores"], 2, 3, 8, 1.0, 1.0, a["acc"], a["out"], a["workspace"], row_len=a["row_len"], stream=0)
+    L.rq_evict_accumulate(a["scores"], 2, 3, 8, 1.0, a.get("decay", 1.0), a["acc"], a["out"], a["workspace"], row_len=a["row_len"], stream=0)
 
 
 def call_select(**kw):
@@ -346,6 +346,11 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu(call):
     """Tensors that are right but for the memory they lie in: their addresses mean nothing to a kernel."""
     with pytest.raises(ValueError, match="on one GPU"):
         call()
+
+
+def test_accumulate_without_history_does_not_look_at_the_old_sums():
+    with pytest.raises(ValueError, match="on one GPU"):         # the only thing wrong here
+        call_accumulate(decay=0.0, acc=zeros(3, dtype=torch.float16))
 
 
 def test_gather_of_an_empty_cache_is_a_noop_for_the_library():
