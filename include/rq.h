@@ -392,9 +392,11 @@ rq_status rq_rotary(const void *x, const rq_strides *x_strides, void *out, const
  *             rounded to fp16: by 2^-11 of itself, or by 2^-25 where it is below 2^-14.
  * (qjl_attention rounds c and n / d to fp16 and scales weights by 2^14 of the true
  * running maximum: the two agree to these roundings, not bit for bit.)  The
- * drafted part, sums and joins are fp32; the output is rounded once.
+ * drafted part, sums and joins are fp32; the output is rounded once.  A row whose
+ * query or whose logits are not finite in fp32 comes out NaN, and no other row does.
  * Supported: d = 128, m % 64 == 0, codes of 1, 2, 3, 4 bits packed or int8, values
- * likewise (RQ_EUNSUPPORTED otherwise); n_nodes <= 1024. */
+ * likewise (RQ_EUNSUPPORTED otherwise); n_nodes <= 1024, n_rep * n_nodes <= 65536,
+ * B * n_kv_heads <= 65535 (RQ_ESIZE). */
 
 /* Device workspace qjl_tree_attention needs (bytes), for the current device; 0 on invalid sizes. */
 size_t qjl_tree_attention_workspace_bytes(int64_t B, int n_kv_heads, int n_rep, int n_nodes, int d, int m, int64_t T);

@@ -471,3 +471,20 @@ def test_single_buffers_are_used_again(rows, m, kbits, vbits):
         kt, vt = vectors(part, KV, T, m, kbits, vbits)
         check(got[b:b + 1], kt, vt, q[b:b + 1], kn[b:b + 1], vn[b:b + 1], None, lens[b * KV:(b + 1) * KV], scale)
     assert torch.equal(got, run(c, q, kn, vn, None, m, T, lens, kbits, vbits, scale))
+
+
+@pytest.mark.parametrize("kbits", [0, 2])
+def test_a_row_beyond_the_range_of_logits_spoils_no_other(kbits):
+    """A query of the largest finite values: its logits pass the fp32 range, its neighbours are as without it."""
+    T, m, n, rep = 500, 128, 5, 4
+    c = compress(1, T, D, m, kbits, 4, 111, kbits > 0)
+    q, kn, vn = drafted(1, n, 1, rep, 112)
+    plain = run(c, q, kn, vn, None, m, T, None, kbits, 4, 0.1)
+    odd = q.clone()
+    odd[0, 3, 2] = torch.finfo(torch.bfloat16).max * q[0, 3, 2].sign()
+    got = run(c, odd, kn, vn, None, m, T, None, kbits, 4, 0.1)
+    torch.cuda.synchronize()
+    assert L.rq_device_error(True) == 0
+    got[0, 3, 2] = plain[0, 3, 2]
+    kt, vt = vectors(c, 1, T, m, kbits, 4)
+    check(got, kt, vt, q, kn, vn, None, None, 0.1)
